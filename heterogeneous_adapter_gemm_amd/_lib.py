@@ -84,6 +84,19 @@ class lora_engine_stats(ctypes.Structure):
         "wait_ms_hit_p99", "wait_ms_miss_p50", "wait_ms_miss_p99", "wait_steps_p99", "wait_steps_max",
         "storage_ms_p50", "storage_ms_p99")]
 
+
+class lora_kv_batch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_heads", "n_kv_heads", "head_dim", "n_seqs", "n_rows", "max_rows",
+                                              "max_blocks", "reserved")] + [
+        ("row_start", _VP), ("ctx_len", _VP), ("page_table", _VP)]
+
+
+class lora_kv_rows(ctypes.Structure):
+    _fields_ = [(n, _VP) for n in ("k", "v", "q", "q_out", "k_out", "v_out")] + [
+        (n, ctypes.c_int64) for n in ("k_stride", "v_stride", "q_stride", "q_out_stride", "k_out_stride",
+                                      "v_out_stride")]
+
+
 _SIGS = {
     "lora_pool_meta_bytes": [ctypes.POINTER(lora_pool_desc), _I64P],
     "lora_pool_create": [ctypes.POINTER(lora_pool_desc), ctypes.POINTER(_VP)],
@@ -114,6 +127,14 @@ _SIGS = {
     "base_gemm": [ctypes.c_int32, _VP, _VP, _VP, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _VP],
     "base_gemm_fp8": [_VP, _VP, _VP, _VP, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _VP],
     "lora_linear_fp8": [_VP, _VP, ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP],
+    "base_gemm_w4": [_VP, _VP, _VP, _VP, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _VP],
+    "lora_linear_w4": [_VP, _VP, ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP, ctypes.c_int32, _VP, _VP],
+    "lora_kv_pages_per_block": [_VP, ctypes.c_int32, ctypes.c_int32, _I32P],
+    "lora_kv_workspace_bytes": [ctypes.POINTER(lora_kv_batch), _I64P],
+    "lora_kv_append": [_VP, ctypes.POINTER(lora_kv_batch), ctypes.POINTER(lora_kv_rows), _VP, ctypes.c_int32,
+                       ctypes.c_int32, ctypes.c_int32, _VP],
+    "lora_kv_attention": [_VP, ctypes.POINTER(lora_kv_batch), _VP, ctypes.c_int64, _VP, ctypes.c_int64,
+                          ctypes.c_float, _VP, ctypes.c_int64, _VP],
     "lora_engine_create": [_VP, ctypes.POINTER(lora_engine_desc), ctypes.POINTER(_VP)],
     "lora_engine_destroy": [_VP],
     "lora_engine_submit": [_VP, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32],
@@ -433,6 +454,42 @@ def base_gemm_fp8(x, w0_code, w0_scale, y, M: int, N: int, K: int, stream=None) 
 def lora_linear_fp8(pool: Pool, plan: Plan, layer: int, proj: int, x, w0_code, w0_scale, y, stream=None) -> None:
     _check(library().lora_linear_fp8(pool.handle, plan.handle, layer, proj, _addr(x), _addr(w0_code),
                                      _addr(w0_scale), _addr(y), _stream(stream)), "lora_linear_fp8")
+
+
+def base_gemm_w4(x, w0_code, w0_scale, y, M: int, N: int, K: int, group: int, stream=None) -> None:
+    _check(library().base_gemm_w4(_addr(x), _addr(w0_code), _addr(w0_scale), _addr(y), M, N, K, group,
+                                  _stream(stream)), "base_gemm_w4")
+
+
+def lora_linear_w4(pool: Pool, plan: Plan, layer: int, proj: int, x, w0_code, w0_scale, group: int, y,
+                   stream=None) -> None:
+    _check(library().lora_linear_w4(pool.handle, plan.handle, layer, proj, _addr(x), _addr(w0_code),
+                                    _addr(w0_scale), group, _addr(y), _stream(stream)), "lora_linear_w4")
+
+
+def lora_kv_pages_per_block(pool: Pool, n_kv_heads: int, head_dim: int) -> int:
+    out = ctypes.c_int32()
+    _check(library().lora_kv_pages_per_block(pool.handle, n_kv_heads, head_dim, ctypes.byref(out)),
+           "lora_kv_pages_per_block")
+    return out.value
+
+
+def lora_kv_workspace_bytes(batch: lora_kv_batch) -> int:
+    out = ctypes.c_int64()
+    _check(library().lora_kv_workspace_bytes(ctypes.byref(batch), ctypes.byref(out)), "lora_kv_workspace_bytes")
+    return out.value
+
+
+def lora_kv_append(pool: Pool, batch: lora_kv_batch, rows: lora_kv_rows, cos_sin=None, rot_dim: int = 0,
+                   rot_positions: int = 0, interleaved: bool = False, stream=None) -> None:
+    _check(library().lora_kv_append(pool.handle, ctypes.byref(batch), ctypes.byref(rows), _addr(cos_sin), rot_dim,
+                                    rot_positions, int(interleaved), _stream(stream)), "lora_kv_append")
+
+
+def lora_kv_attention(pool: Pool, batch: lora_kv_batch, q, q_stride: int, out, out_stride: int, scale: float, workspace,
+                      workspace_bytes: int, stream=None) -> None:
+    _check(library().lora_kv_attention(pool.handle, ctypes.byref(batch), _addr(q), q_stride, _addr(out), out_stride,
+                                       scale, _addr(workspace), workspace_bytes, _stream(stream)), "lora_kv_attention")
 
 
 def base_gemm(dtype: int, x, w0, y, M: int, N: int, K: int, stream=None) -> None:

@@ -23,6 +23,13 @@ struct PoolInfo {
     uint64_t base_id;
 };
 PoolInfo pool_info(const lora_pool* p);
+// The pool's pages, for the KV calls (pages_dev NULL: host-only).
+struct PoolPages {
+    void* pages_dev;
+    int64_t num_pages, page_bytes;
+    int32_t dtype;
+};
+PoolPages pool_pages(const lora_pool* p);
 
 // Decode (BGMV) work partition constants.
 constexpr int kShrinkRowsPerUnit = 4;   // rank-rows of A per shrink workgroup (one wave each)
@@ -173,6 +180,12 @@ hipError_t launch_gemm(int dtype, const void* x, const void* w, void* y, int64_t
 bool gemm_w8_ok(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_w8(const void* x, const void* q, const float* scale, void* y, int64_t M, int64_t N, int64_t K,
                           const int32_t* row_slot, float* ybase, hipStream_t s);
+// 4-bit base: y = x W^T, W[n][k] = scale * (code - zero), codes [N][K / 2] bytes, sz [N][K / group]
+// words (fp16 scale low, fp16 zero high); rows m with row_slot[m] >= 0 go unrounded to ybase.
+// gemm_w4_ok: group 32, 64 or 128, N % 4 == 0, K % 128 == 0, 32-bit byte offsets.
+bool gemm_w4_ok(int64_t M, int64_t N, int64_t K, int32_t group);
+hipError_t launch_gemm_w4(const void* x, const void* q, const void* sz, int32_t group, void* y, int64_t M, int64_t N,
+                          int64_t K, const int32_t* row_slot, float* ybase, hipStream_t s);
 // FP8 base for decode batches (M <= 64, a.n_su > 0): the product, the BGMV shrink and the
 // index copy in one launch, as launch_gemm_shrink (raw_mask as there).
 bool gemm_w8_shrink_fits(int64_t M, int64_t N, int64_t K, int n_su);

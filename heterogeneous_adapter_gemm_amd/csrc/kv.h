@@ -1,0 +1,53 @@
+// Declarations shared by the KV host side (kv.cpp) and its gfx950 kernels
+// (kv_kernels.hip).  Not part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace hagemm {
+
+constexpr int kKvBlock = 16;   // tokens of one slab
+
+// Bytes of one slab: 16 rows of head_dim 4-bit codes and 16 words.
+constexpr int kv_slab_bytes(int head_dim) { return 8 * head_dim + 64; }
+
+// A batch over the pool's KV pages (the C header's lora_kv_batch with the pool's part).
+struct KvArgs {
+    uint8_t* pages;
+    int64_t page_bytes;
+    int32_t num_pages;
+    int32_t heads, kv_heads, group;      // group = heads / kv_heads
+    int32_t n_seqs, n_rows, max_blocks;
+    int32_t pages_per_block, slabs_per_page;
+    const int32_t* row_start;
+    const int32_t* ctx_len;
+    const int32_t* table;
+};
+
+struct KvAppendArgs {
+    const void *q, *k, *v;
+    void *q_out, *k_out, *v_out;         // q_out NULL: no q; k_out, v_out may be NULL
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride, v_out_stride;   // elements
+    const float* cos_sin;                // [positions][rot]: rot / 2 cosines, then sines; NULL: no rotation
+    int32_t rot, interleaved;
+};
+
+// Workgroups that the attention aims at (its work is cut so that about this many share it),
+// and the partial results its workspace holds: a cut sequence has at least two parts, each
+// but its last a whole one, so at most twice as many parts as workgroups aimed at.
+constexpr int kKvUnits = 1024;
+constexpr int kKvSlots = 2 * kKvUnits;
+constexpr int kKvRowTile = 16;           // query rows of one decode unit
+constexpr int kKvPrefillRows = 64;       // query rows of one prefill unit
+constexpr int64_t kv_workspace_bytes(int head_dim, int group, int max_rows) {
+    const int64_t rows = (int64_t)max_rows * group <= kKvRowTile ? kKvRowTile : kKvPrefillRows;
+    return kKvSlots * rows * (head_dim + 2) * 4;
+}
+
+hipError_t launch_kv_append(int head_dim, const KvArgs& b, const KvAppendArgs& a, hipStream_t s);
+// max_rows: the caller's bound on a sequence's rows (chooses kernels only)
+hipError_t launch_kv_attention(int head_dim, const KvArgs& b, const void* q, int64_t q_stride, void* out,
+                               int64_t out_stride, float scale, int32_t max_rows, void* workspace, hipStream_t s);
+
+}  // namespace hagemm

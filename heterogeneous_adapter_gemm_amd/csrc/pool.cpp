@@ -968,6 +968,10 @@ int set_error(int code, const char* fmt, ...) {
 
 int64_t pool_pages_for_rank(const lora_pool* p, int32_t rank) { return (int64_t)rank * p->pages_per_rank; }
 
+PoolPages pool_pages(const lora_pool* p) {
+    return {p->host_only ? nullptr : p->pages_dev, p->num_pages, (int64_t)p->page_elems * p->elem_bytes, p->dtype};
+}
+
 PoolInfo pool_info(const lora_pool* p) {
     PoolInfo i{};
     i.host_only = p->host_only;
@@ -1292,15 +1296,17 @@ namespace {
 // otherwise w0 holds E4M3 codes [d_out][d_in] with w0_scale [d_out] (the FP8 base; bf16 pool).
 // n projections of one layer that share x (n = 1: one lora_linear call): their shrinks run in
 // shared launches, then each projection's base GEMM and expand
+// w0_scale NULL: w0s are in the pool's type; else one projection whose base is FP8 (w4_group 0,
+// fp32 scales) or 4-bit (w4_group: k per scale and zero).
 int linear_impl(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t n, const int32_t* projs, const void* x,
-                const void* const* w0s, const float* w0_scale, void* const* ys, void* stream) {
+                const void* const* w0s, const void* w0_scale, int32_t w4_group, void* const* ys, void* stream) {
     if (!p || !plan || plan->pool != p) return fail(LORA_EINVAL, "plan does not belong to this pool");
     if (p->host_only) return fail(LORA_EINVAL, "host-only pool: no device work");
     if (n < 1 || !projs || !w0s || !ys) return fail(LORA_EINVAL, "no projections");
     if (n > 1 && (n > p->max_multi || n > plan->L.multi))
         return fail(LORA_EINVAL, "%d projections in one call; the pool takes at most %d", n,
                     std::min(p->max_multi, plan->L.multi));
-    if (n > 1 && w0_scale) return fail(LORA_EINVAL, "the FP8 base takes one projection per call");
+    if (n > 1 && w0_scale) return fail(LORA_EINVAL, "a quantised base takes one projection per call");
     const int32_t proj = projs[0];
     const void* w0 = w0s[0];
     void* y = ys[0];
@@ -1322,7 +1328,7 @@ int linear_impl(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t n, c
     // projection: there the call is n single calls
     if (n > 1 && w0 && plan->n_tiles == 0 && gemm_shrink_fits(p->dtype, T, plan->n_su)) {
         for (int32_t i = 0; i < n; ++i) {
-            const int rc = linear_impl(p, plan, layer, 1, projs + i, x, w0s + i, nullptr, ys + i, stream);
+            const int rc = linear_impl(p, plan, layer, 1, projs + i, x, w0s + i, nullptr, 0, ys + i, stream);
             if (rc) return rc;
         }
         return LORA_OK;
@@ -1404,15 +1410,19 @@ int linear_impl(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t n, c
     }
     hipError_t e = hipSuccess;
     const int dt = p->dtype;
-    const bool fp8 = w0_scale != nullptr;
+    const bool w4 = w0_scale != nullptr && w4_group != 0, fp8 = w0_scale != nullptr && !w4;
+    const float* w8_scale = static_cast<const float*>(w0_scale);
     if (fp8 && (dt != LORA_BF16 || !gemm_w8_ok(T, a.d_out, a.d_in) || (uintptr_t)w0_scale % 16))
         return fail(LORA_EINVAL, "FP8 base: needs a bf16 pool, d_in a multiple of 128, d_out of 4, a 16-byte aligned "
                                  "scale and 32-bit byte offsets");
+    if (w4 && (dt != LORA_BF16 || !gemm_w4_ok(T, a.d_out, a.d_in, w4_group) || (uintptr_t)w0_scale % 16))
+        return fail(LORA_EINVAL, "4-bit base: needs a bf16 pool, a group of 32, 64 or 128, d_in a multiple of 128, d_out "
+                                 "of 4, a 16-byte aligned w0_scale and 32-bit byte offsets");
     const bool any = plan->n_groups > 0 || plan->n_tiles > 0;
     float* ybase = any ? reinterpret_cast<float*>(base + L.ybase_bytes_off) : nullptr;
     const int32_t* rs = any ? I(L.row_slot) : nullptr;
     // decode batches: the base GEMM and the BGMV shrink share one launch
-    const bool gemm_done = w0 && a.n_tiles == 0 &&
+    const bool gemm_done = w0 && !w4 && a.n_tiles == 0 &&
                            (fp8 ? gemm_w8_shrink_fits(T, a.d_out, a.d_in, a.n_su) : gemm_shrink_fits(dt, T, a.n_su));
     const PlanStage& ps = p->pstage[plan->stage];
     if (first && !gemm_done) {
@@ -1454,7 +1464,7 @@ int linear_impl(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t n, c
             const void* cps = first ? ps.host_dev : nullptr;
             void* cpd = first ? base : nullptr;
             const int64_t cpn = first ? plan->words : 0;
-            return fp8 ? launch_gemm_w8_shrink(x, w0, w0_scale, y, T, a.d_out, a.d_in, rsh, raw_mask, ybase, ah, cps,
+            return fp8 ? launch_gemm_w8_shrink(x, w0, w8_scale, y, T, a.d_out, a.d_in, rsh, raw_mask, ybase, ah, cps,
                                                cpd, cpn, st)
                        : launch_gemm_shrink(dt, x, w0, y, T, a.d_out, a.d_in, rsh, raw_mask, ybase, ah, cps, cpd, cpn,
                                             st);
@@ -1495,7 +1505,8 @@ int linear_impl(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t n, c
             // rows with an adapter keep the unrounded base for their expand: one rounding in total
             const LoraArgs* seg = plan->n_tiles > 0 ? &ai : nullptr;
             e = timed_launch(p, LORA_K_GEMM, st, [&] {
-                return fp8 ? launch_gemm_w8(x, wi, w0_scale, yi, T, ai.d_out, ai.d_in, rs, ybase_i, st)
+                return w4  ? launch_gemm_w4(x, wi, w0_scale, w4_group, yi, T, ai.d_out, ai.d_in, rs, ybase_i, st)
+                       : fp8 ? launch_gemm_w8(x, wi, w8_scale, yi, T, ai.d_out, ai.d_in, rs, ybase_i, st)
                            : launch_gemm(dt, x, wi, yi, T, ai.d_out, ai.d_in, rs, ybase_i, seg, &fused, st);
             });
             if (e != hipSuccess) return fail(LORA_EHIP, "base_gemm: %s", hipGetErrorString(e));
@@ -1523,18 +1534,25 @@ extern "C" {
 
 int lora_linear(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t proj, const void* x, const void* w0,
                 void* y, void* stream) {
-    return linear_impl(p, plan, layer, 1, &proj, x, &w0, nullptr, &y, stream);
+    return linear_impl(p, plan, layer, 1, &proj, x, &w0, nullptr, 0, &y, stream);
 }
 
 int lora_linear_multi(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t n, const int32_t* projs,
                       const void* x, const void* const* w0, void* const* y, void* stream) {
-    return linear_impl(p, plan, layer, n, projs, x, w0, nullptr, y, stream);
+    return linear_impl(p, plan, layer, n, projs, x, w0, nullptr, 0, y, stream);
 }
 
 int lora_linear_fp8(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t proj, const void* x,
                     const void* w0_code, const float* w0_scale, void* y, void* stream) {
     if (!w0_code || !w0_scale) return fail(LORA_EINVAL, "w0_code and w0_scale are required");
-    return linear_impl(p, plan, layer, 1, &proj, x, &w0_code, w0_scale, &y, stream);
+    return linear_impl(p, plan, layer, 1, &proj, x, &w0_code, w0_scale, 0, &y, stream);
+}
+
+int lora_linear_w4(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t proj, const void* x, const void* w0_code,
+                   const void* w0_scale, int32_t group, void* y, void* stream) {
+    if (!w0_code || !w0_scale) return fail(LORA_EINVAL, "w0_code and w0_scale are required");
+    if (group != 32 && group != 64 && group != 128) return fail(LORA_EINVAL, "group must be 32, 64 or 128");
+    return linear_impl(p, plan, layer, 1, &proj, x, &w0_code, w0_scale, group, &y, stream);
 }
 
 int lora_linear_decode(lora_pool* p, int32_t layer, int32_t proj, const void* x, const void* w0, void* y,
@@ -1596,6 +1614,22 @@ int base_gemm_fp8(const void* x, const void* w0_code, const float* w0_scale, voi
         return fail(LORA_EINVAL, "pointers must be 16-byte aligned");
     hipError_t e = launch_gemm_w8(x, w0_code, w0_scale, y, M, N, K, nullptr, nullptr, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail(LORA_EHIP, "base_gemm_fp8: %s", hipGetErrorString(e));
+    return LORA_OK;
+}
+
+int base_gemm_w4(const void* x, const void* w0_code, const void* w0_scale, void* y, int64_t M, int64_t N, int64_t K,
+                 int32_t group, void* stream) {
+    if (M < 0 || N < 1 || K < 1 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return fail(LORA_EINVAL, "bad sizes");
+    if (group != 32 && group != 64 && group != 128) return fail(LORA_EINVAL, "group must be 32, 64 or 128");
+    if (N % 4 || K % 128) return fail(LORA_EINVAL, "N must be a multiple of 4 and K of 128");
+    if (M == 0) return LORA_OK;
+    if (!gemm_w4_ok(M, N, K, group)) return fail(LORA_EINVAL, "x and w0_code must be below 2^31 bytes");
+    if (!x || !w0_code || !w0_scale || !y) return fail(LORA_EINVAL, "NULL pointer");
+    if ((uintptr_t)x % 16 || (uintptr_t)w0_code % 16 || (uintptr_t)w0_scale % 16 || (uintptr_t)y % 16)
+        return fail(LORA_EINVAL, "pointers must be 16-byte aligned");
+    hipError_t e =
+        launch_gemm_w4(x, w0_code, w0_scale, group, y, M, N, K, nullptr, nullptr, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(LORA_EHIP, "base_gemm_w4: %s", hipGetErrorString(e));
     return LORA_OK;
 }
 

@@ -37,6 +37,48 @@ def device_tensor(arr: np.ndarray, device="cuda"):
     return host_tensor(arr, pin=False).to(device)
 
 
+class KvBatch:
+    """A batch over the pool's KV pages (lora_kv_batch in the C header): device int32 tensors
+    row_start [n_seqs + 1], ctx_len [n_seqs] and page_table [n_seqs, max_blocks, pages per block]
+    (one layer's), n_rows rows of q, k and v, at most max_rows of one sequence (None: n_rows).
+    The tensors are read when the kernels run: a caller may write new lengths or pages into
+    them between calls, and between replays of a captured one."""
+
+    def __init__(self, n_heads: int, n_kv_heads: int, head_dim: int, row_start, ctx_len, page_table, n_rows: int,
+                 max_rows: Optional[int] = None):
+        import torch
+        for name, t, dim in (("row_start", row_start, 1), ("ctx_len", ctx_len, 1), ("page_table", page_table, 3)):
+            if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous int32 tensor of {dim} dimension(s)")
+        n_seqs = ctx_len.shape[0]
+        if row_start.shape[0] != n_seqs + 1 or page_table.shape[0] != n_seqs:
+            raise ValueError(f"{n_seqs} lengths, {row_start.shape[0]} row starts, {page_table.shape[0]} page tables")
+        if len({row_start.device, ctx_len.device, page_table.device}) != 1:
+            raise ValueError("row_start, ctx_len and page_table must be on one device")
+        self.row_start, self.ctx_len, self.page_table = row_start, ctx_len, page_table
+        self.pages_per_block = page_table.shape[2]
+        self.n_rows = n_rows
+        self.c = L.lora_kv_batch(n_heads, n_kv_heads, head_dim, n_seqs, n_rows, n_rows if max_rows is None else max_rows,
+                                 page_table.shape[1], 0, row_start.data_ptr(), ctx_len.data_ptr(),
+                                 page_table.data_ptr())
+
+    def rows(self, name: str, t, heads: int) -> int:
+        """The row stride of t, checked to be this batch's rows of so many heads."""
+        import torch
+        c = self.c
+        if t.device != self.row_start.device or t.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be bfloat16 on {self.row_start.device}")
+        if t.dim() == 2 and t.shape[1] == heads * c.head_dim:
+            inner = t.stride(1) == 1
+        elif t.dim() == 3 and t.shape[1:] == (heads, c.head_dim):
+            inner = t.stride(2) == 1 and (heads == 1 or t.stride(1) == c.head_dim)
+        else:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, not [rows, {heads}, {c.head_dim}] or [rows, {heads * c.head_dim}]")
+        if t.shape[0] != self.n_rows or not inner:
+            raise ValueError(f"{name}: {self.n_rows} rows of contiguous heads are needed")
+        return t.stride(0) if self.n_rows > 1 else heads * c.head_dim
+
+
 class DevicePool:
     def __init__(self, dtype: int, page_elems: int, num_pages: int, free_order: Optional[Sequence[int]],
                  n_layers: int, d_in: Sequence[int], d_out: Sequence[int], max_slots: int, max_rank: int,
@@ -147,6 +189,64 @@ class DevicePool:
 
     def linear_fp8(self, plan: L.Plan, layer: int, proj: int, x, w0_code, w0_scale, y, stream=None) -> None:
         L.lora_linear_fp8(self.pool, plan, layer, proj, x, w0_code, w0_scale, y, stream)
+
+    def linear_w4(self, plan: L.Plan, layer: int, proj: int, x, w0_code, w0_scale, group: int, y, stream=None) -> None:
+        L.lora_linear_w4(self.pool, plan, layer, proj, x, w0_code, w0_scale, group, y, stream)
+
+    # -- keys and values in the pages ----------------------------------------------
+    def kv_pages_per_block(self, n_kv_heads: int, head_dim: int) -> int:
+        """Pages of 16 tokens' keys and values in one layer."""
+        return L.lora_kv_pages_per_block(self.pool, n_kv_heads, head_dim)
+
+    def kv_workspace(self, batch: KvBatch):
+        """A workspace for kv_attention; calls that may overlap need one each."""
+        import torch
+        return torch.empty(L.lora_kv_workspace_bytes(batch.c), dtype=torch.uint8, device=batch.row_start.device)
+
+    def _kv_check(self, batch: KvBatch, stream):
+        import torch
+        dev = batch.row_start.device
+        if self.pages is None or dev != self.pages.device:
+            raise ValueError(f"the batch is on {dev}, the pool on {self.pages.device if self.pages is not None else None}")
+        need = self.kv_pages_per_block(batch.c.n_kv_heads, batch.c.head_dim)
+        if batch.pages_per_block != need:
+            raise ValueError(f"page_table has {batch.pages_per_block} pages a block, {need} are needed")
+        return torch.cuda.current_stream(dev) if stream is None else stream
+
+    def kv_append(self, batch: KvBatch, k, v, q=None, q_out=None, k_out=None, v_out=None, cos_sin=None,
+                  interleaved: bool = False, stream=None) -> None:
+        """Append the rows' keys and values to their pages; q, k turned by cos_sin [positions, rot_dim]."""
+        import torch
+        st = self._kv_check(batch, stream)
+        c, r = batch.c, L.lora_kv_rows()
+        for name, t, heads in (("k", k, c.n_kv_heads), ("v", v, c.n_kv_heads), ("q", q, c.n_heads),
+                               ("q_out", q_out, c.n_heads), ("k_out", k_out, c.n_kv_heads),
+                               ("v_out", v_out, c.n_kv_heads)):
+            if t is not None:
+                setattr(r, name, t.data_ptr())
+                setattr(r, name + "_stride", batch.rows(name, t, heads))
+        pos = rot = 0
+        if cos_sin is not None:
+            if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or \
+                    cos_sin.device != batch.row_start.device:
+                raise ValueError("cos_sin must be a contiguous float32 [positions, rot_dim] tensor on the batch's device")
+            pos, rot = cos_sin.shape
+        with torch.cuda.device(batch.row_start.device):
+            L.lora_kv_append(self.pool, c, r, cos_sin, rot, pos, interleaved, st)
+
+    def kv_attention(self, batch: KvBatch, q, out, scale: Optional[float] = None, workspace=None, stream=None) -> None:
+        """Attention of the batch's rows (q already turned) over the pages; scale None: head_dim ** -0.5."""
+        import torch
+        st = self._kv_check(batch, stream)
+        c = batch.c
+        if workspace is None:
+            raise ValueError("kv_attention needs a workspace (kv_workspace)")
+        if workspace.device != batch.row_start.device or not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous and on the batch's device")
+        with torch.cuda.device(batch.row_start.device):
+            L.lora_kv_attention(self.pool, c, q, batch.rows("q", q, c.n_heads), out, batch.rows("out", out, c.n_heads),
+                                c.head_dim ** -0.5 if scale is None else scale, workspace,
+                                workspace.numel() * workspace.element_size(), st)
 
     def linear_decode(self, layer: int, proj: int, x, w0, y, token_slot, stream=None) -> None:
         L.lora_linear_decode(self.pool, layer, proj, x, w0, y, token_slot, stream)

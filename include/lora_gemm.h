@@ -218,8 +218,8 @@ int lora_pool_release(lora_pool* pool, int32_t slot);
 /* KV blocks share the pool ("S-LoRA: Serving Thousands of Concurrent LoRA
  * Adapters", Unified paging): take n pages from the front of the free list
  * (all or none; ENOPAGES), or return pages (each must be a KV page, listed
- * once; EINVAL otherwise) to the tail in the given order.  The library never
- * reads or writes KV page contents. */
+ * once; EINVAL otherwise) to the tail in the given order.  Only the lora_kv_*
+ * calls, told so by their page table, read or write KV page contents. */
 int lora_pool_alloc_kv(lora_pool* pool, int32_t n_pages, int32_t* out_pages);
 int lora_pool_free_kv(lora_pool* pool, int32_t n_pages, const int32_t* pages);
 
@@ -363,6 +363,122 @@ int base_gemm_fp8(const void* x, const void* w0_code, const float* w0_scale, voi
  * the pool is not bf16 or the shapes break base_gemm_fp8's requirements. */
 int lora_linear_fp8(lora_pool* pool, const lora_plan* plan, int32_t layer, int32_t proj, const void* x,
                     const void* w0_code, const float* w0_scale, void* y, void* stream);
+
+/*
+ * 4-bit base: the base weight in 4-bit codes with a scale and a zero point
+ * per group of consecutive inputs (the form in which quantized bases with
+ * 16-bit adapters are most often held).
+ *   W0[n][k] = scale[n][k / group] * (code[n][k] - zero[n][k / group])
+ * w0_code [N][K / 2] bytes, code[n][k] 0..15 in the low (k even) or high half
+ * of byte k / 2 of row n; w0_scale [N][K / group] pairs of fp16 (scale, then
+ * zero; the zero need not be whole); group 32, 64 or 128.  x and y are bf16.
+ *   y[M][N] = x[M][K] * W0[N][K]^T, fp32 accumulation (the matrix cores run on
+ * the codes, which are exact in bf16; scale and zero are applied to fp32 sums
+ * of a group), output rounded to bf16 once.
+ * Requires N % 4 == 0, K % 128 == 0, 16-byte aligned pointers, M * K * 2 and
+ * N * K / 2 below 2^31.  M = 0 is a no-op.  Errors: EINVAL, EHIP. */
+int base_gemm_w4(const void* x, const void* w0_code, const void* w0_scale, void* y, int64_t M, int64_t N, int64_t K,
+                 int32_t group, void* stream);
+
+/* lora_linear with a 4-bit base (bf16 pool): y = x W0^T + delta with W0 as in
+ * base_gemm_w4 (w0_code [d_out][d_in / 2], w0_scale [d_out][d_in / group]
+ * pairs); the delta is lora_linear's, and rows with an adapter are rounded
+ * once.  Errors as lora_linear, and EINVAL when the pool is not bf16 or the
+ * shapes break base_gemm_w4's requirements. */
+int lora_linear_w4(lora_pool* pool, const lora_plan* plan, int32_t layer, int32_t proj, const void* x,
+                   const void* w0_code, const void* w0_scale, int32_t group, void* y, void* stream);
+
+/*
+ * Keys and values in the pool's KV pages, 4 bits each ("S-LoRA: Serving
+ * Thousands of Concurrent LoRA Adapters", Unified paging: KV blocks share the
+ * adapters' pages).  lora_kv_append puts a step's new rows there, turning
+ * queries and keys by their position on the way; lora_kv_attention reads them.
+ *
+ * Form.  A row of head_dim values is held as lo + step * code, code 0..15, in
+ * head_dim / 2 bytes and one 32-bit word (bf16 step in the low half, bf16 lo in
+ * the high half): lo the row's least value, step = (greatest - lo) / 15 rounded
+ * to bf16, code the nearest (ties to even).  A row that holds an infinity or
+ * NaN reads back as NaN.  Keys are rounded to bf16 after the rotation and before
+ * this.
+ *
+ * Place.  A block is 16 consecutive tokens of one sequence in one layer.  The
+ * keys (or values) of one KV head in a block are one slab of 8 head_dim + 64
+ * bytes: codes, then the 16 words.  Slab 2 h of a block is head h's keys, slab
+ * 2 h + 1 its values; page j of a block holds slabs j n .. j n + n - 1 one after
+ * another, n = min(page bytes / slab bytes, 2 n_kv_heads), so a block takes
+ * lora_kv_pages_per_block pages (any pages of the pool, such as
+ * lora_pool_alloc_kv gives).  Code order inside a slab:
+ *   keys    row-major [16][head_dim / 2]; in each little-endian 32-bit word of 8
+ *           values, bits 4 k .. 4 k + 3 are value 2 k and bits 4 k + 16 .. value
+ *           2 k + 1 (k 0..3)
+ *   values  [16][8][head_dim / 64][2] 16-bit units: unit (i, p, g, b) holds
+ *           values i head_dim / 16 + 4 g .. + 3 (lowest bits first) of token
+ *           2 p + b
+ *
+ * A batch: sequences whose rows (of q, k, v, out) are [row_start[s],
+ * row_start[s + 1]) and which hold ctx_len[s] tokens once this step's rows are
+ * appended, the rows being the last ones: row j of n is at position ctx_len[s]
+ * - n + j.  The arrays are device memory and are read by the kernels only, so
+ * a captured call follows their contents at replay.  Rows behind
+ * row_start[n_seqs] belong to no sequence and stay as they are.  Contents that do
+ * not fit are bounded by the kernels: row numbers to [0, n_rows], lengths to [0,
+ * 16 max_blocks]; a row whose position is negative is not appended and its
+ * attention output is zero; tokens of a page outside the pool are not kept and
+ * are left out of the attention.
+ *   head_dim     64, 128 or 256;  n_heads a multiple of n_kv_heads (query head h
+ *                reads KV head h / (n_heads / n_kv_heads))
+ *   max_rows     the most rows of one sequence: chooses kernels and the
+ *                workspace's size, never which rows are computed
+ *   page_table   [n_seqs][max_blocks][pages per block], of one layer; entries
+ *                past a sequence's last block are not read
+ */
+typedef struct lora_kv_batch {
+    int32_t n_heads, n_kv_heads, head_dim;
+    int32_t n_seqs, n_rows, max_rows, max_blocks;
+    int32_t reserved;               /* 0 */
+    const int32_t* row_start;       /* device [n_seqs + 1], not decreasing, from 0 */
+    const int32_t* ctx_len;         /* device [n_seqs] */
+    const int32_t* page_table;      /* device */
+} lora_kv_batch;
+
+/* Rows of lora_kv_append, bf16 [n_rows][heads][head_dim] with a row stride in
+ * elements (a multiple of 8, at least heads * head_dim), 16-byte aligned. */
+typedef struct lora_kv_rows {
+    const void *k, *v;              /* n_kv_heads heads */
+    const void* q;                  /* n_heads heads, or NULL */
+    void* q_out;                    /* q turned (may be q itself), or NULL with q */
+    void *k_out, *v_out;            /* the rows as the cache now holds them (may be k, v), or NULL */
+    int64_t k_stride, v_stride, q_stride, q_out_stride, k_out_stride, v_out_stride;
+} lora_kv_rows;
+
+/* Pages of one block of 16 tokens.  EINVAL: pool not bf16, head_dim not 64,
+ * 128 or 256, or a page that holds no slab. */
+int lora_kv_pages_per_block(const lora_pool* pool, int32_t n_kv_heads, int32_t head_dim, int32_t* out);
+
+/* Device workspace lora_kv_attention needs for a batch (from head_dim, the
+ * head counts and max_rows only).  Nothing in it needs to start at zero.  Calls
+ * that overlap need one each. */
+int lora_kv_workspace_bytes(const lora_kv_batch* batch, int64_t* out_bytes);
+
+/* Append: the rows' keys and values to their pages, and q to q_out, the first
+ * rot_dim values of every q and k head turned by their position's angles: pairs
+ * (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved, (a, b) -> (a cos - b
+ * sin, b cos + a sin).  cos_sin: device fp32 [rot_positions][rot_dim], rot_dim / 2
+ * cosines then as many sines; NULL with rot_dim 0: no rotation.  rot_dim a
+ * multiple of 16 up to head_dim; rot_positions at least 16 max_blocks.  Bytes of a
+ * block past its last token stay as they are.  Two rows of one batch must not
+ * name the same token's place.  Errors: EINVAL, EHIP. */
+int lora_kv_append(lora_pool* pool, const lora_kv_batch* batch, const lora_kv_rows* rows, const float* cos_sin,
+                   int32_t rot_dim, int32_t rot_positions, int32_t interleaved, void* stream);
+
+/* Attention of the batch's rows over the pages: out row = softmax over the
+ * tokens at positions up to the row's own of scale * q . key, times the values.
+ * q (already turned) and out: bf16 [n_rows][n_heads][head_dim] with row strides as
+ * in lora_kv_rows.  Scores, softmax sums and outputs are held in fp32; the output
+ * is rounded once.  The same inputs give the same bits.  scale > 0 and finite.
+ * Errors: EINVAL, EHIP. */
+int lora_kv_attention(lora_pool* pool, const lora_kv_batch* batch, const void* q, int64_t q_stride, void* out,
+                      int64_t out_stride, float scale, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * Engine layer: memory management and scheduling around the pool.
