@@ -33,16 +33,16 @@ struct KvAppendArgs {
     int32_t rot, interleaved;
 };
 
-// Workgroups that the attention aims at (its work is cut so that about this many share it),
-// and the partial results its workspace holds: a cut sequence has at least two parts, each
-// but its last a whole one, so at most twice as many parts as workgroups aimed at.
-constexpr int kKvUnits = 1024;
-constexpr int kKvSlots = 2 * kKvUnits;
-constexpr int kKvRowTile = 16;           // query rows of one decode unit
-constexpr int kKvPrefillRows = 64;       // query rows of one prefill unit
+constexpr int kKvRowTile = 16;           // query rows of a decode segment
+constexpr int kKvPrefillRows = 64;       // query rows of a prefill segment
+// Waves that share the attention's work, as many as run at once by their registers: on each of
+// 256 CUs 16 (head_dim 64), 12 (128) or 8 (256).  A prefill worker is a workgroup of four.
+constexpr int kv_workers(int head_dim) { return 1024 * (head_dim == 64 ? 4 : head_dim == 128 ? 3 : 2); }
+// An entry a worker, and two partial results of a row tile of fp32 sums and (m, l) each.
 constexpr int64_t kv_workspace_bytes(int head_dim, int group, int max_rows) {
-    const int64_t rows = (int64_t)max_rows * group <= kKvRowTile ? kKvRowTile : kKvPrefillRows;
-    return kKvSlots * rows * (head_dim + 2) * 4;
+    const int64_t few = (int64_t)kv_workers(head_dim) * (36 + 2 * kKvRowTile * (head_dim + 2) * 4);
+    const int64_t many = (int64_t)kv_workers(head_dim) / 4 * (36 + 2 * kKvPrefillRows * (head_dim + 2) * 4);
+    return (int64_t)max_rows * group <= kKvRowTile || few > many ? few : many;
 }
 
 hipError_t launch_kv_append(int head_dim, const KvArgs& b, const KvAppendArgs& a, hipStream_t s);

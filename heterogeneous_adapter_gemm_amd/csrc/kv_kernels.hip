@@ -12,6 +12,9 @@
 //   values  [i = 16][token pair][4 values][token of the pair]: a lane has head_dim / 16
 //           values of four consecutive tokens, two tokens side by side in each 32-bit word
 // No byte is shared by two tokens' codes, so tokens can be appended one by one.
+#include <algorithm>
+#include <type_traits>
+
 #include "common.h"
 #include "kv.h"
 
@@ -20,7 +23,6 @@ namespace {
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
-typedef unsigned u32pair __attribute__((ext_vector_type(2)));
 
 // ---------------------------------------------------------------- sequences
 
@@ -37,11 +39,11 @@ __device__ __forceinline__ KvSeq kv_seq(const KvArgs& b, int s) {
     return q;
 }
 
-// The page of (sequence, block, slab), or -1 outside the pool.
-__device__ __forceinline__ int kv_page(const KvArgs& b, int s, int block, int slab) {
-    const int p = b.table[((int64_t)s * b.max_blocks + block) * b.pages_per_block + slab / b.slabs_per_page];
-    return p >= 0 && p < b.num_pages ? p : -1;
+// The table's entry for (sequence, block, slab); any number may stand there.
+__device__ __forceinline__ const int32_t* kv_entry(const KvArgs& b, int s, int block, int slab) {
+    return b.table + ((int64_t)s * b.max_blocks + block) * b.pages_per_block + slab / b.slabs_per_page;
 }
+__device__ __forceinline__ bool kv_page_ok(const KvArgs& b, int page) { return (uint32_t)page < (uint32_t)b.num_pages; }
 
 // ---------------------------------------------------------------- append
 
@@ -166,8 +168,8 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvArgs b, KvAppendArgs a
              pack(z, bf16_t{}));
     }
     const int slab = 2 * h + (kind == 2), r = pos % kKvBlock;
-    const int page = kv_page(b, s, pos / kKvBlock, slab);
-    if (page < 0) return;   // a page outside the pool: the row is not kept
+    const int page = *kv_entry(b, s, pos / kKvBlock, slab);
+    if (!kv_page_ok(b, page)) return;   // a page outside the pool: the row is not kept
     uint8_t* at = b.pages + page * b.page_bytes + (slab % b.slabs_per_page) * kv_slab_bytes(D);
     if (kind == 1) {
         uint32_t w = 0;
@@ -191,121 +193,159 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvArgs b, KvAppendArgs a
 
 // ---------------------------------------------------------------- attention: the work's cut
 
-// Every workgroup finds its own piece of work from the device's lengths, so the launch does
-// not depend on them (a captured call follows them).  Sequences are cut into row tiles of RB
-// query rows and into parts of C steps of 32 tokens, C the same for all, so that about
-// kKvUnits parts come out (but no part is shorter than min_steps).
+// The work is a line of steps (32 tokens each) of all segments, one after another: a segment is
+// a row tile (rb query rows of one KV head) of a sequence, its steps those of the sequence's
+// tokens, tiles and heads in turn (heads innermost).  Workers (waves or workgroups) take equal
+// pieces of the line, so that short and long sequences keep all of them busy alike; a segment
+// that a border cuts leaves partial results, which a second launch joins.  Every workgroup
+// finds its piece from the device's lengths, so the launch does not depend on them (a captured
+// call follows them).
 enum KvClass { kKvAll = 0, kKvFew = 1, kKvMany = 2 };   // sequences: all, of at most kKvRowTile query rows, of more
 
 struct KvCut {
-    int rb, cls, min_steps;
+    int rb_shift, cls, workers;
 };
-
-struct KvUnit {
-    int s, h, tile, part, parts, slot;   // slot: this part's (or the first part's) place in the workspace
-    int steps_per_part;
-    KvSeq q;
-};
-
-__device__ __forceinline__ int kv_tiles(const KvArgs& b, const KvCut& cut, const KvSeq& q) {
-    const int64_t rows = (int64_t)q.rows * b.group;
-    if (rows == 0 || (cut.cls == kKvFew && rows > kKvRowTile) || (cut.cls == kKvMany && rows <= kKvRowTile)) return 0;
-    return (int)((rows + cut.rb - 1) / cut.rb);
-}
 
 __device__ __forceinline__ int kv_steps(int tokens) { return (tokens + 31) >> 5; }
 
-// Unit `index` of the cut (merge: unit `index` of the row tiles, its first part's slot).
-// Every thread of the 256 calls it; false past the last unit.
-__device__ __forceinline__ bool kv_find(const KvArgs& b, const KvCut& cut, int64_t index, bool merge, KvUnit* u) {
-    __shared__ int64_t sums[4][2];
-    __shared__ int found[4];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int64_t work = 0;
-    for (int s = threadIdx.x; s < b.n_seqs; s += 256) {
-        const KvSeq q = kv_seq(b, s);
-        work += (int64_t)kv_tiles(b, cut, q) * kv_steps(q.len);
-    }
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) work += __shfl_xor(work, m, 64);
-    if (lane == 0) sums[wave][0] = work;
-    if (threadIdx.x == 0) found[0] = -1;
-    __syncthreads();
-    work = (sums[0][0] + sums[1][0] + sums[2][0] + sums[3][0]) * b.kv_heads;
-    const int64_t per = max((work + kKvUnits - 1) / kKvUnits, (int64_t)cut.min_steps);
-    const int C = (int)min(per, (int64_t)(1 << 30));
-    const int h = (int)(index % b.kv_heads);
-    const int64_t want = index / b.kv_heads;
-    int64_t base = 0, slot_base = 0;   // units and slots of the sequences before this round's
-    for (int s0 = 0; s0 < b.n_seqs; s0 += 256) {
-        const int s = s0 + threadIdx.x;
-        KvSeq q{0, 0, 0};
-        int tiles = 0, parts = 1;
-        if (s < b.n_seqs) {
-            q = kv_seq(b, s);
-            tiles = kv_tiles(b, cut, q);
-            parts = max(1, (kv_steps(q.len) + C - 1) / C);
-        }
-        const int64_t n = (int64_t)tiles * (merge ? 1 : parts), k = parts > 1 ? (int64_t)tiles * parts : 0;
-        int64_t in = n, ik = k;   // inclusive sums over the wave, then over the workgroup
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-            const int64_t a = __shfl_up(in, m, 64), c = __shfl_up(ik, m, 64);
-            if (lane >= m) {
-                in += a;
-                ik += c;
-            }
-        }
-        __syncthreads();   // (the sums of the round before have been read)
-        if (lane == 63) {
-            sums[wave][0] = in;
-            sums[wave][1] = ik;
-        }
-        __syncthreads();
-        int64_t all = 0, allk = 0;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            if (w < wave) {
-                in += sums[w][0];
-                ik += sums[w][1];
-            }
-            all += sums[w][0];
-            allk += sums[w][1];
-        }
-        const int64_t mine = want - base - (in - n);
-        if (mine >= 0 && mine < n) {
-            found[0] = s;
-            found[1] = (int)mine;
-            found[2] = parts;
-            found[3] = (int)((slot_base + ik - k + (merge ? mine * parts : mine)) * b.kv_heads + h);
-        }
-        base += all;
-        slot_base += allk;
-        if (want < base) break;
-    }
-    __syncthreads();
-    if (found[0] < 0) return false;
-    u->s = found[0];
-    u->h = h;
-    u->parts = found[2];
-    u->tile = merge ? found[1] : found[1] / u->parts;
-    u->part = merge ? 0 : found[1] % u->parts;
-    u->slot = found[3];
-    u->steps_per_part = C;
-    u->q = kv_seq(b, u->s);
-    return true;
+// (row tile, head) pairs of a sequence, and steps of each (at least one: rows without a token
+// have to be written too)
+__device__ __forceinline__ int kv_pairs(const KvArgs& b, const KvCut& cut, const KvSeq& q) {
+    const int64_t rows = (int64_t)q.rows * b.group;
+    if ((cut.cls == kKvFew && rows > kKvRowTile) || (cut.cls == kKvMany && rows <= kKvRowTile)) return 0;
+    return (int)((rows + (1 << cut.rb_shift) - 1) >> cut.rb_shift) * b.kv_heads;
 }
+__device__ __forceinline__ int kv_seg_steps(const KvSeq& q) { return max(1, kv_steps(q.len)); }
+
+// Inclusive sum over the wave's lanes.
+__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) {
+        const int64_t o = __shfl_up(v, x, 64);
+        if ((int)(threadIdx.x & 63) >= x) v += o;
+    }
+    return v;
+}
+
+// The line, as a workgroup keeps it: before[i] = steps before sequence i m (m sequences a
+// thread), before[256] all of them.
+struct KvLine {
+    int64_t before[257];
+    int64_t sums[4];
+};
+
+__device__ __forceinline__ void kv_line(const KvArgs& b, const KvCut& cut, KvLine& line) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int m = (b.n_seqs + 255) >> 8;
+    const int s0 = threadIdx.x * m, s1 = min(s0 + m, b.n_seqs);
+    int64_t mine = 0;
+    for (int s = s0; s < s1; ++s) {
+        const KvSeq q = kv_seq(b, s);
+        mine += (int64_t)kv_pairs(b, cut, q) * kv_seg_steps(q);
+    }
+    int64_t in = wave_scan(mine);
+    if (lane == 63) line.sums[wave] = in;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 3; ++w)
+        if (w < wave) in += line.sums[w];
+    line.before[threadIdx.x] = in - mine;
+    if (threadIdx.x == 255) line.before[256] = in;
+    __syncthreads();
+}
+
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v & 0xFFFFFFFF)) |
+                     (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32);
+}
+
+// Where a worker's piece begins: total steps in equal pieces, the first total % workers one longer.
+struct KvPieces {
+    int64_t size, longer;
+    int workers;
+    __device__ __forceinline__ KvPieces(int64_t total, int most) {
+        workers = (int)min(total, (int64_t)most);
+        // (at most a few thousand workers: the quotient fits a double exactly enough, then is put right)
+        size = workers > 0 ? (int64_t)((double)total / workers) : 0;
+        if (size * workers > total) --size;
+        if (workers > 0 && total - size * workers >= workers) ++size;
+        longer = total - size * workers;
+    }
+    __device__ __forceinline__ int64_t at(int w) const { return w * size + min((int64_t)w, longer); }
+    // the worker whose piece holds step x
+    __device__ __forceinline__ int holder(int64_t x) const {
+        const int64_t first = longer * (size + 1);
+        int w = x < first ? (int)((double)x / (double)(size + 1)) : (int)(longer + (int64_t)((double)(x - first) / (double)size));
+        w = min(w, workers - 1);
+        if (at(w) > x) --w;
+        if (w + 1 < workers && at(w + 1) <= x) ++w;
+        return w;
+    }
+};
+
+// A place on the line: pair `pair` of sequence s, `off` of its `steps` steps in.  All uniform
+// over the wave.
+struct KvPlace {
+    int s, pair, pairs, off, steps;
+    KvSeq q;
+
+    __device__ __forceinline__ void enter(const KvArgs& b, const KvCut& cut, int seq) {
+        s = seq;
+        q = kv_seq(b, s);
+        pairs = kv_pairs(b, cut, q);
+        steps = kv_seg_steps(q);
+    }
+    // pos below the line's end
+    __device__ __forceinline__ void seek(const KvArgs& b, const KvCut& cut, const KvLine& line, int64_t pos) {
+        const int lane = threadIdx.x & 63;
+        // the last of the 256 threads' sequences that begin at or before pos
+        int last = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) last += __popcll(__ballot(line.before[64 * i + lane] <= pos));
+        const int m = (b.n_seqs + 255) >> 8;
+        int64_t left = pos - uniform64(line.before[last - 1]);
+        enter(b, cut, (last - 1) * m);
+        while (left >= (int64_t)pairs * steps) {
+            left -= (int64_t)pairs * steps;
+            enter(b, cut, s + 1);
+        }
+        pair = (int)((double)left / steps);
+        if ((int64_t)pair * steps > left) --pair;
+        if (left - (int64_t)pair * steps >= steps) ++pair;
+        off = (int)(left - (int64_t)pair * steps);
+        pair = __builtin_amdgcn_readfirstlane(pair);
+        off = __builtin_amdgcn_readfirstlane(off);
+    }
+    // the segment after this one (one with steps must follow)
+    __device__ __forceinline__ void next(const KvArgs& b, const KvCut& cut) {
+        off = 0;
+        if (++pair < pairs) return;
+        pair = 0;
+        do enter(b, cut, s + 1);
+        while (pairs == 0);
+    }
+};
 
 // ---------------------------------------------------------------- attention: one wave
 
 // The two bf16 halves 16 + code of nibble k of both 16-bit halves of w: a nibble in the top
 // four bits of bf16's seven mantissa bits counts ones above 16, so the codes need no
-// conversion, only their place.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int k) {
+// conversion, only their place.  mask and ones: 0x00780078 and 0x41804180, in registers (a
+// three-operand and-or takes no constants of its own).
+struct CodeConst {
+    uint32_t mask = 0x00780078u, ones = 0x41804180u;
+    __device__ __forceinline__ CodeConst() { asm volatile("" : "+v"(mask), "+v"(ones)); }
+};
+__device__ __forceinline__ uint32_t code_pair(const CodeConst& c, uint32_t w, int k) {
     const uint32_t s = k == 0 ? w << 3 : k == 1 ? w >> 1 : k == 2 ? w >> 5 : w >> 9;
-    return (s & 0x00780078u) | 0x41804180u;
+    return (s & c.mask) | c.ones;
 }
 
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{lo, hi}, bf16x2_t));
+}
+
+// Over the four lanes that share a query row (lane % 16).
 __device__ __forceinline__ float max_lg(float v) {
     auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
@@ -319,75 +359,106 @@ __device__ __forceinline__ float sum_lg(float v) {
     return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
-template <int W>
-__device__ __forceinline__ void ld_words(const uint8_t* p, uint32_t (&o)[W]) {
-    if constexpr (W == 2) {
-        const u32x2 v = *reinterpret_cast<const u32x2*>(p);
-        o[0] = v[0];
-        o[1] = v[1];
-    } else {
-#pragma unroll
-        for (int j = 0; j < W / 4; ++j) {
-            const u32x4 v = ld16(p + 16 * j);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[4 * j + i] = v[i];
-        }
-    }
+// 4 bytes per lane straight into LDS (lane i -> lds + 4 i)
+__device__ __forceinline__ void global_load_lds4(const void* p, void* lds) {
+    __builtin_amdgcn_global_load_lds(const_cast<void*>(p), (lds_vptr)lds, 4, 0, 0);
 }
 
-// One step's keys and values of a wave: two slabs of each.
+// s_waitcnt lgkmcnt(0), the other counters unconstrained
+__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
+
+// A wave's place for one step in LDS: the codes of two slabs of keys and two of values, then
+// their words.
 template <int D>
-struct KvTile {
-    static constexpr int W = D / 32;
-    uint32_t k[2][W], v[2][W];
-    u32x4 kw[2], vw[2];
+struct KvStage {
+    static constexpr int kCodes = 32 * D, kBytes = kCodes + 256;
 };
 
-// A wave's 16 query rows against tokens, 32 at a time.  Lane (li, lg) = (lane % 16, lane / 16)
-// holds everything of query row li: of the scores those of tokens 4 lg .. 4 lg + 3 of both
-// slabs, of the output the values 4 lg D / 16 .. + D / 4.
-//   scores   S^T = K Q^T: matrix operations on the codes themselves (16 + code, exact in bf16),
-//            then s = step * (acc - 16 sum(q)) + lo * sum(q), all fp32
-//   weights  p = 2^(c s - m); m is raised, and everything summed so far scaled down, only
-//            when a score passes it by more than 8 (the sums' scale needs no closer bound)
+// Sum over the lanes of a 16-lane row that are a multiple of ROWS apart.
+template <int ROWS>
+__device__ __forceinline__ float sum_cols(float v) {
+    auto ror = [](float x, auto n) {
+        return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x120 + decltype(n)::value, 0xf, 0xf, true));
+    };
+    if constexpr (ROWS <= 8) v += ror(v, std::integral_constant<int, 8>{});
+    if constexpr (ROWS <= 4) v += ror(v, std::integral_constant<int, 4>{});
+    if constexpr (ROWS <= 2) v += ror(v, std::integral_constant<int, 2>{});
+    if constexpr (ROWS <= 1) v += ror(v, std::integral_constant<int, 1>{});
+    return v;
+}
+template <int ROWS>
+__device__ __forceinline__ float max_cols(float v) {
+    auto ror = [](float x, auto n) {
+        return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x120 + decltype(n)::value, 0xf, 0xf, true));
+    };
+    if constexpr (ROWS <= 8) v = fmaxf(v, ror(v, std::integral_constant<int, 8>{}));
+    if constexpr (ROWS <= 4) v = fmaxf(v, ror(v, std::integral_constant<int, 4>{}));
+    if constexpr (ROWS <= 2) v = fmaxf(v, ror(v, std::integral_constant<int, 2>{}));
+    if constexpr (ROWS <= 1) v = fmaxf(v, ror(v, std::integral_constant<int, 1>{}));
+    return v;
+}
+
+// A wave's query rows against tokens, 32 at a time.  A matrix operation has 16 columns for
+// query rows; where there are fewer rows, each takes COLS = 16 / ROWS columns, lane (li, lg) =
+// (lane % 16, lane / 16) being in column li of row li % ROWS.  The columns of a row have the
+// same scores and share the work on them: SUB of them take every SUB-th part of the tokens (the
+// others' weights are zeros in their column), and with SPLIT each of those is a pair, one for
+// either half of the weights; the columns' outputs are summed at the end.
+//   scores   S^T = K Q^T: matrix operations on the codes themselves (16 + code, exact in bf16);
+//            a lane gets tokens 4 lg .. 4 lg + 3 of both slabs and picks its own, then s = step *
+//            (acc - 16 sum(q)) + lo * sum(q), all fp32
+//   weights  p = 2^(c (s - m)); m is raised, and everything summed so far scaled down, only
+//            when a score passes it by more than 8 / c (the sums' scale needs no closer bound)
 //   output   O^T += V^T P'^T with P' = p step in two bf16 halves (high and the rest, so its
-//            error is 2^-17, below fp32 sums' worth of tokens) and V's codes as 16 + code;
-//            z = sum p (lo - 16 step) takes the rest
-template <int D>
+//            error is 2^-17) and V's codes as 16 + code; z = sum p (lo - 16 step) takes the
+//            rest.  A lane gets the values 4 lg D / 16 .. + D / 4.
+template <int D, int SUB, bool SPLIT>
 struct KvWave {
-    static constexpr int W = D / 32, NE = D / 16;
+    static constexpr int W = D / 32, NE = D / 16, COLS = SPLIT ? 2 * SUB : SUB, ROWS = 16 / COLS, NEL = 8 / SUB;
     uint32_t q[W][4];
     float qsum;
     f32x4 o[NE];
     float m, l, z;
     int limit;          // tokens this lane's row sees
     int limit_all;      // tokens every row of the tile sees
+    int h, s, last_block;
+    CodeConst cc;
 
-    __device__ __forceinline__ void load_q(const KvArgs& b, const KvUnit& u, const bf16_t* qp, int64_t stride, int row0) {
-        const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
-        const int rows = u.q.rows * b.group;
-        const int r = row0 + li;
+    static __device__ __forceinline__ int row() { return (threadIdx.x & 15) % ROWS; }
+    static __device__ __forceinline__ int col() { return (threadIdx.x & 15) / ROWS; }
+    static __device__ __forceinline__ int part() { return SPLIT ? col() % 2 : 0; }      // 1: the weights' low half
+    static __device__ __forceinline__ int sub() { return SPLIT ? col() / 2 : col(); }
+
+    // ROWS query rows from row0 on, of one KV head of sequence seq
+    __device__ __forceinline__ void load_q(const KvArgs& b, int seq, const KvSeq& sq, int head, const bf16_t* qp,
+                                           int64_t stride, int row0) {
+        const int lg = (threadIdx.x & 63) >> 4;
+        const int rows = sq.rows * b.group;
+        const int r = row0 + row();
+        h = head;
+        s = seq;
+        last_block = (sq.len + kKvBlock - 1) / kKvBlock - 1;
         qsum = 0.f;
         if (r < rows) {
-            const bf16_t* p = qp + (int64_t)(u.q.r0 + r / b.group) * stride +
-                              (int64_t)(u.h * b.group + r % b.group) * D + lg * (D / 4);
+            const bf16_t* p = qp + (int64_t)(sq.r0 + r / b.group) * stride +
+                              (int64_t)(h * b.group + r % b.group) * D + lg * (D / 4);
 #pragma unroll
-            for (int s = 0; s < W; ++s) {
-                const u32x4 v = ld16(p + 8 * s);
+            for (int i = 0; i < W; ++i) {
+                const u32x4 v = ld16(p + 8 * i);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    q[s][i] = v[i];
-                    qsum += bf16_lo(v[i]) + bf16_hi(v[i]);
+                for (int j = 0; j < 4; ++j) {
+                    q[i][j] = v[j];
+                    qsum += bf16_lo(v[j]) + bf16_hi(v[j]);
                 }
             }
         } else {
 #pragma unroll
-            for (int s = 0; s < W; ++s)
+            for (int i = 0; i < W; ++i)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) q[s][i] = 0;
+                for (int j = 0; j < 4; ++j) q[i][j] = 0;
         }
         qsum = sum_lg(qsum);
-        const int first = u.q.len - u.q.rows + 1;   // tokens the sequence's first row sees
+        const int first = sq.len - sq.rows + 1;   // tokens the sequence's first row sees
         limit = r < rows ? first + r / b.group : 0;
         limit_all = first + row0 / b.group;
         m = -INFINITY;
@@ -396,55 +467,58 @@ struct KvWave {
         for (int e = 0; e < NE; ++e) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    __device__ __forceinline__ void step(const KvTile<D>& t, int tok0, int bad, int len, float c) {
-        const int lg = (threadIdx.x & 63) >> 4;
+    // One step: kc and vc the lane's codes of two slabs, kw and vw the words of its NEL tokens.
+    __device__ __forceinline__ void step(const uint32_t (&kc)[2][W], const uint32_t (&vc)[2][W], const uint32_t (&kw)[NEL],
+                                         const uint32_t (&vw)[NEL], int tok0, int bad, float c, float raise) {
+        const int lg = (threadIdx.x & 63) >> 4, sb = sub();
         f32x4 sc[2];
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
             const float init = -16.f * qsum;
             sc[a] = f32x4{init, init, init, init};
+        }
 #pragma unroll
-            for (int s = 0; s < W; ++s) {
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
                 u32x4 kf, qf;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    kf[i] = code_pair(t.k[a][s], i);
-                    qf[i] = q[s][i];
+                for (int j = 0; j < 4; ++j) {
+                    kf[j] = code_pair(cc, kc[a][i], j);
+                    qf[j] = q[i][j];
                 }
                 sc[a] = mma_step(kf, qf, sc[a], bf16_t{});
             }
+        float x[NEL], st[NEL], zp[NEL];
+#pragma unroll
+        for (int k = 0; k < NEL; ++k) {
+            if constexpr (SUB == 1) x[k] = sc[k / 4][k % 4];
+            else if constexpr (SUB == 2) x[k] = sb ? sc[1][k] : sc[0][k];
+            else if constexpr (SUB == 4) x[k] = sb & 2 ? (sb & 1 ? sc[1][2 + k] : sc[1][k]) : (sb & 1 ? sc[0][2 + k] : sc[0][k]);
+            else x[k] = sb & 4 ? (sb & 2 ? (sb & 1 ? sc[1][3] : sc[1][2]) : (sb & 1 ? sc[1][1] : sc[1][0]))
+                               : (sb & 2 ? (sb & 1 ? sc[0][3] : sc[0][2]) : (sb & 1 ? sc[0][1] : sc[0][0]));
+            x[k] = fmaf(x[k], bf16_lo(kw[k]), bf16_hi(kw[k]) * qsum);
+            st[k] = bf16_lo(vw[k]);
+            zp[k] = fmaf(-16.f, st[k], bf16_hi(vw[k]));
         }
-        float st[2][4], zp[2][4];
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sc[a][i] = (sc[a][i] * bf16_lo(t.kw[a][i]) + bf16_hi(t.kw[a][i]) * qsum) * c;
-                st[a][i] = bf16_lo(t.vw[a][i]);
-                zp[a][i] = bf16_hi(t.vw[a][i]) - 16.f * st[a][i];
-            }
-        if (tok0 + 32 > limit_all || bad) {
+        if (__builtin_expect(tok0 + 32 > limit_all || bad, 0)) {
             // tokens that a row does not see count nothing, whatever the pages hold there
 #pragma unroll
-            for (int a = 0; a < 2; ++a)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = tok0 + 16 * a + 4 * lg + i;
-                    if (tok >= limit || ((bad >> a) & 1)) {
-                        sc[a][i] = -INFINITY;
-                        st[a][i] = 0.f;
-                        zp[a][i] = 0.f;
-                    }
+            for (int k = 0; k < NEL; ++k) {
+                const int a = (sb * NEL + k) / 4, tok = tok0 + 16 * a + 4 * lg + (sb * NEL + k) % 4;
+                if (tok >= limit || ((bad >> a) & 1)) {
+                    x[k] = -INFINITY;
+                    st[k] = 0.f;
+                    zp[k] = 0.f;
                 }
+            }
         }
-        float top = sc[0][0];
+        float top = x[0];
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[a][i]);
-        if (__ballot(top > m + 8.f)) {
-            const float mn = fmaxf(m, max_lg(top));
-            const float al = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+        for (int k = 1; k < NEL; ++k) top = fmaxf(top, x[k]);
+        if (__ballot(top > m + raise)) {
+            const float mn = fmaxf(m, max_cols<ROWS>(max_lg(top)));
+            const float al = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(c * (m - mn));
             m = mn;
             l *= al;
             z *= al;
@@ -453,260 +527,514 @@ struct KvWave {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[e][i] *= al;
         }
-        const float ref = m == -INFINITY ? 0.f : m;
-        u32x4 ph, pl;
+        const float ref = m == -INFINITY ? 0.f : -c * m;
+        float w[NEL];
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
+        for (int k = 0; k < NEL; ++k) {
+            const float p = __builtin_amdgcn_exp2f(fmaf(x[k], c, ref));
+            l += p;
+            z = fmaf(p, zp[k], z);
+            w[k] = p * st[k];
+        }
+        // the weights' halves, at this column's tokens
+        u32x4 ph{0, 0, 0, 0}, pl{0, 0, 0, 0};
+        if constexpr (NEL == 1) {
+            const uint32_t hi = pack2(w[0], 0.f), lo = pack2(w[0] - bf16_lo(hi), 0.f);
+            const int at = 16 * (sb & 1);
+            const uint32_t a = (SPLIT && part() ? lo : hi) << at, b = lo << at;
 #pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-                const float p0 = __builtin_amdgcn_exp2f(sc[a][i] - ref), p1 = __builtin_amdgcn_exp2f(sc[a][i + 1] - ref);
-                l += p0;
-                l += p1;
-                z = fmaf(p0, zp[a][i], z);
-                z = fmaf(p1, zp[a][i + 1], z);
-                const float w0 = p0 * st[a][i], w1 = p1 * st[a][i + 1];
-                const uint32_t hi = pack_bf16(w0, w1);
-                ph[2 * a + i / 2] = hi;
-                pl[2 * a + i / 2] = pack_bf16(w0 - bf16_lo(hi), w1 - bf16_hi(hi));
+            for (int y = 0; y < 4; ++y) {
+                ph[y] = sb >> 1 == y ? a : 0;
+                if constexpr (!SPLIT) pl[y] = sb >> 1 == y ? b : 0;
             }
+        } else {
+#pragma unroll
+            for (int k = 0; k < NEL; k += 2) {
+                const uint32_t hi = pack2(w[k], w[k + 1]);
+                const uint32_t lo = pack2(w[k] - bf16_lo(hi), w[k + 1] - bf16_hi(hi));
+                const uint32_t a = SPLIT && part() ? lo : hi;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    if (y % (NEL / 2) != k / 2) continue;
+                    const bool mine = SUB == 1 || sb == y / (NEL / 2);
+                    ph[y] = mine ? a : 0;
+                    if constexpr (!SPLIT) pl[y] = mine ? lo : 0;
+                }
+            }
+        }
+        u32x4 vf[NE];
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
             constexpr int NH = W / 2;
-            u32x4 vf;
 #pragma unroll
             for (int a = 0; a < 2; ++a)
 #pragma unroll
-                for (int p = 0; p < 2; ++p) vf[2 * a + p] = code_pair(t.v[a][p * NH + e / 4], e % 4);
-            o[e] = mma_step(vf, ph, o[e], bf16_t{});
-            o[e] = mma_step(vf, pl, o[e], bf16_t{});
+                for (int p = 0; p < 2; ++p) vf[e][2 * a + p] = code_pair(cc, vc[a][p * NH + e / 4], e % 4);
+            o[e] = mma_step(vf[e], ph, o[e], bf16_t{});
+            if constexpr (!SPLIT) {
+                // (a block behind, so that no operation waits for the one before it)
+                if (e > 0) o[e - 1] = mma_step(vf[e - 1], pl, o[e - 1], bf16_t{});
+            }
         }
+        if constexpr (!SPLIT) o[NE - 1] = mma_step(vf[NE - 1], pl, o[NE - 1], bf16_t{});
     }
 
-    // steps first, first + stride, ... below end
-    __device__ __forceinline__ void run(const KvArgs& b, const KvUnit& u, int first, int end, int stride, float c) {
+    // Steps first .. end - 1.  Their slabs go straight to LDS, two steps ahead of the one at work
+    // (lds0 and lds1 in turn), so that the loads in flight take no registers: a step is read into
+    // registers as a whole, and its place given to the step after the next.
+    __device__ __forceinline__ void run(const KvArgs& b, uint8_t* lds0, uint8_t* lds1, int first, int end, float c) {
         const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
-        const int n = end > first ? (end - first + stride - 1) / stride : 0;
-        const int lane_off = li * (D / 2) + lg * (D / 8);
-        const int ks = 2 * u.h, vs = 2 * u.h + 1;
+        const int n = end - first;
+        if (n <= 0) return;
+        const float raise = 8.f / c;
+        const int ks = 2 * h, vs = 2 * h + 1;
         const int64_t koff = (int64_t)(ks % b.slabs_per_page) * kv_slab_bytes(D);
         const int64_t voff = (int64_t)(vs % b.slabs_per_page) * kv_slab_bytes(D);
-        const int last_block = (u.q.len - 1) / kKvBlock;
-        KvTile<D> t[2];
-        int bad[2] = {0, 0};
-        int pk = 0, pv = 0;   // lane 2 j + a: pages of slab a of step j of the 32 steps at hand
+        constexpr int kCodes = KvStage<D>::kCodes, kLoads = kCodes / 1024 + 1;
+        // lane 4 j + x: page of slab x (keys 0, 1, values 0, 1) of step j of 16
         auto pages = [&](int j0) {
-            const int st = first + (j0 + (lane >> 1)) * stride;
-            const int blk = 2 * st + (lane & 1);
-            pk = pv = -1;
-            if (j0 + (lane >> 1) < n && blk <= last_block) {
-                pk = kv_page(b, u.s, blk, ks);
-                pv = kv_page(b, u.s, blk, vs);
-            }
+            const int j = j0 + (lane >> 2), blk = 2 * (first + j) + (lane & 1);
+            return j < n && blk <= last_block ? *kv_entry(b, s, blk, lane & 2 ? vs : ks) : -1;
         };
-        auto load = [&](int j, KvTile<D>& d, int& bd) {
-            bd = 0;
+        // a lane's word of slab lg
+        const int64_t word_at = (lg < 2 ? koff : voff) + 8 * D + li * 4;
+        // bit a of the result: slab a has no page
+        auto load = [&](int pg, int word_page, int j, uint8_t* to) {
+            const uint8_t* at[4];
+            int bad = 0;
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                const int k = __builtin_amdgcn_readlane(pk, (2 * j + a) & 63);
-                const int v = __builtin_amdgcn_readlane(pv, (2 * j + a) & 63);
-                if (k < 0 || v < 0) bd |= 1 << a;
-                const uint8_t* kp = b.pages + max(k, 0) * b.page_bytes + koff;
-                const uint8_t* vp = b.pages + max(v, 0) * b.page_bytes + voff;
-                ld_words(kp + lane_off, d.k[a]);
-                d.kw[a] = ld16(kp + 8 * D + 16 * lg);
-                ld_words(vp + lane_off, d.v[a]);
-                d.vw[a] = ld16(vp + 8 * D + 16 * lg);
+            for (int x = 0; x < 4; ++x) {
+                const int page = __builtin_amdgcn_readlane(pg, 4 * j + x);
+                const bool ok = kv_page_ok(b, page);
+                bad |= !ok << (x & 1);
+                at[x] = b.pages + (ok ? page : 0) * b.page_bytes + (x < 2 ? koff : voff);
+            }
+            if constexpr (D == 64) {
+                // two slabs a load, in order; a lane's codes of slab x are 8 bytes
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    global_load_lds16((lane < 32 ? at[2 * i] : at[2 * i + 1]) + (lane & 31) * 16, to + 1024 * i);
+            } else {
+                // each lane its own codes, 16 bytes at a time
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int i = 0; i < D / 128; ++i)
+                        global_load_lds16(at[x] + li * (D / 2) + lg * (D / 8) + 16 * i, to + (x * (D / 128) + i) * 1024);
+            }
+            global_load_lds4(b.pages + (kv_page_ok(b, word_page) ? word_page : 0) * b.page_bytes + word_at, to + kCodes);
+            return bad;
+        };
+        // a lane's tokens in a step, as word numbers of the keys' (values') 32
+        const int sb = sub(), word = (sb * NEL) / 4 * 16 + 4 * lg + (sb * NEL) % 4;
+        auto read = [&](const uint8_t* from, uint32_t (&kc)[2][W], uint32_t (&vc)[2][W], uint32_t (&kw)[NEL],
+                        uint32_t (&vw)[NEL]) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                uint32_t (&d)[W] = x < 2 ? kc[x & 1] : vc[x & 1];
+                if constexpr (D == 64) {
+                    const u32x2 u = *reinterpret_cast<const u32x2*>(from + x * 512 + li * 32 + lg * 8);
+                    d[0] = u[0];
+                    d[1] = u[1];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 128; ++i) {
+                        const u32x4 u = ld16(from + (x * (D / 128) + i) * 1024 + lane * 16);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) d[4 * i + y] = u[y];
+                    }
+                }
+            }
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(from + kCodes) + word;
+#pragma unroll
+            for (int k = 0; k < NEL; ++k) {
+                kw[k] = w[k / 4 * 16 + k % 4];
+                vw[k] = w[32 + k / 4 * 16 + k % 4];
             }
         };
-        if (n == 0) return;
-        pages(0);
-        load(0, t[0], bad[0]);
+        auto page_of_word = [&](int pg, int j) { return __builtin_amdgcn_ds_bpermute(4 * (4 * j + lg), pg); };
+        int pg = pages(0), pg_next = -1;
+        int bad[2];
+        bad[0] = load(pg, page_of_word(pg, 0), 0, lds0);
+        bad[1] = n > 1 ? load(pg, page_of_word(pg, 1), 1, lds1) : 0;
+#pragma unroll 1
         for (int j = 0; j < n; j += 2) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 if (j + x >= n) break;
-                if (j + x + 1 < n) {
-                    if (((j + x + 1) & 31) == 0) pages(j + x + 1);
-                    load((j + x + 1) & 31, t[1 - x], bad[1 - x]);
+                // this step's loads have landed (of the ones after them, the next step's alone are out)
+                if (j + x + 1 < n) wait_vmcnt<kLoads>();
+                else wait_vmcnt<0>();
+                uint32_t kc[2][W], vc[2][W], kw[NEL], vw[NEL];
+                read(x ? lds1 : lds0, kc, vc, kw, vw);
+                const int bad_now = bad[x];
+                if (j + x + 2 < n) {
+                    if (((j + x + 2) & 15) == 0) pg = pg_next;
+                    const int wp = page_of_word(pg, (j + x + 2) & 15);
+                    wait_lgkm0();   // the step is in registers: its place is free
+                    if (((j + x) & 15) == 0) pg_next = pages(j + x + 16);
+                    bad[x] = load(pg, wp, (j + x + 2) & 15, x ? lds1 : lds0);
                 }
-                step(t[x], 32 * (first + (j + x) * stride), bad[x], u.q.len, c);
+                step(kc, vc, kw, vw, 32 * (first + j + x), bad_now, c, raise);
             }
         }
     }
 
+    // the sums over a row's lanes and columns
     __device__ __forceinline__ void finish() {
-        l = sum_lg(l);
-        z = sum_lg(z);
+        if (part()) l = z = 0.f;   // (the other half's column has counted them)
+        l = sum_cols<ROWS>(sum_lg(l));
+        z = sum_cols<ROWS>(sum_lg(z));
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[e][i] = sum_cols<ROWS>(o[e][i]);
     }
-};
 
-// Where row r of a tile's results go: the output, or the unit's slot of the workspace.
-struct KvOut {
-    bf16_t* out;
-    int64_t stride;
-    float* part;   // [slots][RB][D], then [slots][RB][2]
-};
-
-template <int D, int RB>
-__device__ __forceinline__ float* part_row(float* part, int slot, int r) {
-    return part + ((int64_t)slot * RB + r) * D;
-}
-template <int D, int RB>
-__device__ __forceinline__ float* part_ml(float* part, int slot, int r) {
-    return part + (int64_t)kKvSlots * RB * D + ((int64_t)slot * RB + r) * 2;
-}
-
-// Few query rows: the four waves share a part's tokens, step by step in turn, and their sums
-// meet in LDS.  Bound by reading the cache once.
-template <int D>
-__global__ __launch_bounds__(256) void kv_decode_kernel(KvArgs b, const bf16_t* q, int64_t q_stride, KvOut w, float c,
-                                                        KvCut cut) {
-    __shared__ float so[4][16][D + 4];
-    __shared__ float sm[4][16][3];
-    KvUnit u;
-    if (!kv_find(b, cut, blockIdx.x, false, &u)) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, lg = lane >> 4;
-    const int rows = u.q.rows * b.group, row0 = u.tile * 16;
-    KvWave<D> wv;
-    wv.load_q(b, u, q, q_stride, row0);
-    // steps up to the last token that the tile's last row sees
-    const int last = min(rows, row0 + 16) - 1;
-    const int seen = max(0, u.q.len - u.q.rows + 1 + last / b.group);
-    const int s0 = u.part * u.steps_per_part, s1 = min(kv_steps(seen), s0 + u.steps_per_part);
-    wv.run(b, u, s0 + wave, s1, 4, c);
-    wv.finish();
-    if (lg == 0) {
-        sm[wave][li][0] = wv.m;
-        sm[wave][li][1] = wv.l;
-        sm[wave][li][2] = wv.z;
-    }
-    constexpr int NE = D / 16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < NE; e += 4) {
-            const f32x4 v{wv.o[e][i], wv.o[e + 1][i], wv.o[e + 2][i], wv.o[e + 3][i]};
-            *reinterpret_cast<f32x4*>(&so[wave][li][(4 * lg + i) * NE + e]) = v;
-        }
-    __syncthreads();
-    // 16 threads a row, D / 16 values each
-    const int r = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * NE;
-    if (row0 + r >= rows) return;
-    float m = -INFINITY;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) m = fmaxf(m, sm[x][r][0]);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f, acc[NE];
-#pragma unroll
-    for (int e = 0; e < NE; ++e) acc[e] = 0.f;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        // (a wave whose tokens were all masked has m = -inf and sums of zero)
-        const float f = sm[x][r][0] == -INFINITY ? (sm[x][r][1] == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(sm[x][r][0] - ref);
-        l += f * sm[x][r][1];
-#pragma unroll
-        for (int e = 0; e < NE; ++e) acc[e] += f * (so[x][r][d0 + e] + sm[x][r][2]);
-    }
-    if (u.parts > 1) {
-        float* p = part_row<D, kKvRowTile>(w.part, u.slot, r) + d0;
-#pragma unroll
-        for (int e = 0; e < NE; e += 4) *reinterpret_cast<f32x4*>(p + e) = f32x4{acc[e], acc[e + 1], acc[e + 2], acc[e + 3]};
-        if (d0 == 0) {
-            float* ml = part_ml<D, kKvRowTile>(w.part, u.slot, r);
-            ml[0] = m;
-            ml[1] = l;
-        }
-        return;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees no token is zero
-    bf16_t* o = w.out + (int64_t)(u.q.r0 + (row0 + r) / b.group) * w.stride +
-                (int64_t)(u.h * b.group + (row0 + r) % b.group) * D + d0;
-#pragma unroll
-    for (int e = 0; e < NE; e += 4) {
-        u32x2 v;
-        v[0] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-        v[1] = pack_bf16(acc[e + 2] * inv, acc[e + 3] * inv);
-        *reinterpret_cast<u32x2*>(o + e) = v;
-    }
-}
-
-// Many query rows: each of the four waves has 16 of the tile's 64 rows and goes over all the
-// part's tokens.
-template <int D>
-__global__ __launch_bounds__(256) void kv_prefill_kernel(KvArgs b, const bf16_t* q, int64_t q_stride, KvOut w, float c,
-                                                         KvCut cut) {
-    KvUnit u;
-    if (!kv_find(b, cut, blockIdx.x, false, &u)) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, lg = lane >> 4;
-    const int rows = u.q.rows * b.group, row0 = u.tile * kKvPrefillRows + 16 * wave;
-    if (row0 >= rows) return;
-    KvWave<D> wv;
-    wv.load_q(b, u, q, q_stride, row0);
-    const int last = min(rows, row0 + 16) - 1;
-    const int seen = max(0, u.q.len - u.q.rows + 1 + last / b.group);
-    const int s0 = u.part * u.steps_per_part, s1 = min(kv_steps(seen), s0 + u.steps_per_part);
-    wv.run(b, u, s0, s1, 1, c);
-    wv.finish();
-    const int r = row0 + li;
-    if (r >= rows) return;
-    constexpr int NE = D / 16;
-    const int rt = 16 * wave + li;
-    if (u.parts > 1) {
-        float* p = part_row<D, kKvPrefillRows>(w.part, u.slot, rt);
+    // the row's results as a part: sums and (m, l)
+    __device__ __forceinline__ void put_part(float* p, float* ml) const {
+        const int lg = (threadIdx.x & 63) >> 4;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int e = 0; e < NE; e += 4)
                 *reinterpret_cast<f32x4*>(p + (4 * lg + i) * NE + e) =
-                    f32x4{wv.o[e][i] + wv.z, wv.o[e + 1][i] + wv.z, wv.o[e + 2][i] + wv.z, wv.o[e + 3][i] + wv.z};
+                    f32x4{o[e][i] + z, o[e + 1][i] + z, o[e + 2][i] + z, o[e + 3][i] + z};
         if (lg == 0) {
-            float* ml = part_ml<D, kKvPrefillRows>(w.part, u.slot, rt);
-            ml[0] = wv.m;
-            ml[1] = wv.l;
+            ml[0] = m;
+            ml[1] = l;
         }
-        return;
     }
-    const float inv = wv.l == 0.f ? 0.f : 1.f / wv.l;
-    bf16_t* o = w.out + (int64_t)(u.q.r0 + r / b.group) * w.stride + (int64_t)(u.h * b.group + r % b.group) * D;
+
+    // the row's results, divided, to the output
+    __device__ __forceinline__ void store(bf16_t* out) const {
+        const int lg = (threadIdx.x & 63) >> 4;
+        const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees no token is zero
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < NE; e += 4) {
+                u32x2 v;
+                v[0] = pack2((o[e][i] + z) * inv, (o[e + 1][i] + z) * inv);
+                v[1] = pack2((o[e + 2][i] + z) * inv, (o[e + 3][i] + z) * inv);
+                *reinterpret_cast<u32x2*>(out + (4 * lg + i) * NE + e) = v;
+            }
+    }
+};
+
+// What the sums of a part (of scale m, weight l) count for at scale top >= m.  A part without
+// tokens has m = -inf and sums of zero; a part of NaN scores m = -inf and l = NaN.
+__device__ __forceinline__ float part_factor(float m, float l, float top, float c) {
+    return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(c * (m - top));
+}
+
+// Where results go: the output, or (a segment cut by a border) the workspace: an entry per
+// worker and its `last` once more, then [2 workers][rb][D] sums and [2 workers][rb][2] (m, l).  A worker has at most two
+// cut segments: one that began before its piece (slot 2 w) and one that ends after it (2 w + 1).
+struct KvOut {
+    bf16_t* out;
+    int64_t stride;
+    uint8_t* ws;
+    int workers;    // the launch's, which place the parts
+};
+// The segment that begins in a worker's piece and ends after it: its parts are this worker's
+// (first) to last's; where the four waves of a workgroup are all inside the segment, their
+// joined part is the first one's.  last = -1: no such segment.
+struct KvMerge {
+    int last, row0, rows, r0, h;
+    int inside0, inside1;           // workgroups [inside0, inside1) have one joined part each
+    int pad;
+};
+static_assert(sizeof(KvMerge) == 32, "workspace layout");
+
+__device__ __forceinline__ void put_merge(const KvOut& w, int worker, const KvMerge& e) {
+    reinterpret_cast<KvMerge*>(w.ws)[worker] = e;
+    reinterpret_cast<int*>(w.ws + (int64_t)w.workers * sizeof(KvMerge))[worker] = e.last;
+}
+__device__ __forceinline__ float* part_base(const KvOut& w) {
+    return reinterpret_cast<float*>(w.ws + (int64_t)w.workers * (sizeof(KvMerge) + 4));
+}
+template <int D>
+__device__ __forceinline__ float* part_row(const KvOut& w, int rb, int slot, int r) {
+    return part_base(w) + ((int64_t)slot * rb + r) * D;
+}
+template <int D>
+__device__ __forceinline__ float* part_ml(const KvOut& w, int rb, int slot, int r) {
+    return part_base(w) + (int64_t)2 * w.workers * rb * D + ((int64_t)slot * rb + r) * 2;
+}
+
+template <int D>
+__device__ __forceinline__ bf16_t* out_row(const KvArgs& b, const KvOut& w, int r0, int h, int r) {
+    return w.out + (int64_t)(r0 + r / b.group) * w.stride + (int64_t)(h * b.group + r % b.group) * D;
+}
+
+// Few query rows.  Workers are waves, each with all of its piece's segments by itself; where a
+// whole workgroup's piece is inside one segment its waves' sums meet in LDS, so that long
+// sequences leave a part a workgroup.  Bound by reading the cache once.
+template <int D, int SUB, bool SPLIT>
+__global__ __launch_bounds__(256, D == 256 ? 2 : 3) void kv_decode_kernel(KvArgs b, const bf16_t* q, int64_t q_stride,
+                                                                          KvOut w, float c, KvCut cut) {
+    using Wave = KvWave<D, SUB, SPLIT>;
+    constexpr int NE = D / 16, RB = Wave::ROWS;
+    constexpr int kStage = KvStage<D>::kBytes, kSums = RB * (D + 4) * 4;
+    // (once the steps are done, a stage holds two waves' sums)
+    constexpr int kHalf = 4 * kStage > 2 * kSums ? 4 * kStage : 2 * kSums;
+    __shared__ __attribute__((aligned(1024))) uint8_t stage0[kHalf];
+    __shared__ __attribute__((aligned(1024))) uint8_t stage1[kHalf];
+    __shared__ float sm[4][RB][3];
+    __shared__ KvLine line;
+    kv_line(b, cut, line);
+    const int lane = threadIdx.x & 63, lg = lane >> 4, row = Wave::row();
+    const bool first_col = Wave::col() == 0;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wg = blockIdx.x, worker = 4 * wg + wave;
+    const KvPieces pieces(uniform64(line.before[256]), cut.workers);
+    int64_t pos = pieces.at(min(worker, pieces.workers));
+    const int64_t end = pieces.at(min(worker + 1, pieces.workers));
+    const int64_t wg_pos = pieces.at(min(4 * wg, pieces.workers)), wg_end = pieces.at(min(4 * wg + 4, pieces.workers));
+    KvMerge entry{-1, 0, 0, 0, 0, 0, 0, 0};
+    bool inside = false;
+    KvPlace at;
+    Wave wv;
+    if (wg_pos < wg_end) {
+        at.seek(b, cut, line, wg_pos);
+        inside = wg_pos + (at.steps - at.off) >= wg_end;
+        if (inside) at.off += (int)(pos - wg_pos);
+        else if (pos < end) at.seek(b, cut, line, pos);
+    }
+    const int64_t seg0 = pos - at.off;    // (where the first segment begins)
+    while (pos < end) {
+        const int h = at.pair % b.kv_heads, row0 = at.pair / b.kv_heads * RB, rows = at.q.rows * b.group;
+        const int stop = (int)min((int64_t)at.steps, at.off + (end - pos));
+        // steps up to the last token that the tile's last row sees
+        const int seen = max(0, at.q.len - at.q.rows + 1 + (min(rows, row0 + RB) - 1) / b.group);
+        wv.load_q(b, at.s, at.q, h, q, q_stride, row0);
+        wv.run(b, stage0 + wave * kStage, stage1 + wave * kStage, at.off, min(kv_steps(seen), stop), c);
+        wv.finish();
+        const int64_t begin = pos - at.off;
+        if (at.off == 0 && stop < at.steps) {
+            // it begins here and is cut: its last worker is the one whose piece holds its last step
+            const int64_t over = begin + at.steps;
+            const int last = pieces.holder(over - 1);
+            int in0 = pieces.at(4 * wg) == begin ? wg : wg + 1, in1 = last >> 2;
+            if (pieces.at(min(4 * in1 + 4, pieces.workers)) == over) ++in1;
+            if (in0 >= in1) in0 = in1 = (last + 4) >> 2;
+            if (!(inside && begin == wg_pos && over == wg_end))
+                entry = KvMerge{last, row0, min(RB, rows - row0), at.q.r0, h, in0, in1, 0};
+        }
+        if (inside) break;
+        if (first_col && row0 + row < rows) {
+            if (at.off == 0 && stop == at.steps)
+                wv.store(out_row<D>(b, w, at.q.r0, h, row0 + row));
+            else
+                wv.put_part(part_row<D>(w, RB, 2 * worker + (at.off == 0), row), part_ml<D>(w, RB, 2 * worker + (at.off == 0), row));
+        }
+        pos += stop - at.off;
+        if (pos < end) at.next(b, cut);
+    }
+    if (lane == 0) put_merge(w, worker, entry);
+    if (!inside) return;
+
+    // the four waves' sums of one segment (a wave without steps has none)
+    if (pos >= end) {
+        wv.m = -INFINITY;
+        wv.l = wv.z = 0.f;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) wv.o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    auto sums = [&](int x, int row, int d) {
+        return reinterpret_cast<float*>((x < 2 ? stage0 : stage1) + (x & 1) * kSums) + row * (D + 4) + d;
+    };
+    __syncthreads();   // (every wave has read its last step)
+    if (first_col) {
+        if (lg == 0) {
+            sm[wave][row][0] = wv.m;
+            sm[wave][row][1] = wv.l;
+            sm[wave][row][2] = wv.z;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < NE; e += 4) {
+                const f32x4 v{wv.o[e][i], wv.o[e + 1][i], wv.o[e + 2][i], wv.o[e + 3][i]};
+                *reinterpret_cast<f32x4*>(sums(wave, row, (4 * lg + i) * NE + e)) = v;
+            }
+    }
+    __syncthreads();
+    // 16 threads a row, D / 16 values each
+    const int r = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * NE;
+    const int h = at.pair % b.kv_heads, row0 = at.pair / b.kv_heads * RB, rows = at.q.rows * b.group;
+    if (r >= RB || row0 + r >= rows) return;
+    float m = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) m = fmaxf(m, sm[x][r][0]);
+    float l = 0.f, acc[NE];
+#pragma unroll
+    for (int e = 0; e < NE; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const float g = part_factor(sm[x][r][0], sm[x][r][1], m, c);
+        l += g * sm[x][r][1];
+#pragma unroll
+        for (int e = 0; e < NE; ++e) acc[e] += g * (*sums(x, r, d0 + e) + sm[x][r][2]);
+    }
+    const int64_t begin = seg0;
+    if (begin == wg_pos && begin + at.steps == wg_end) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        bf16_t* o = out_row<D>(b, w, at.q.r0, h, row0 + r) + d0;
 #pragma unroll
         for (int e = 0; e < NE; e += 4) {
             u32x2 v;
-            v[0] = pack_bf16((wv.o[e][i] + wv.z) * inv, (wv.o[e + 1][i] + wv.z) * inv);
-            v[1] = pack_bf16((wv.o[e + 2][i] + wv.z) * inv, (wv.o[e + 3][i] + wv.z) * inv);
-            *reinterpret_cast<u32x2*>(o + (4 * lg + i) * NE + e) = v;
+            v[0] = pack2(acc[e] * inv, acc[e + 1] * inv);
+            v[1] = pack2(acc[e + 2] * inv, acc[e + 3] * inv);
+            *reinterpret_cast<u32x2*>(o + e) = v;
         }
+    } else {
+        const int slot = 2 * (4 * wg) + (begin == wg_pos);
+        float* p = part_row<D>(w, RB, slot, r) + d0;
+#pragma unroll
+        for (int e = 0; e < NE; e += 4)
+            *reinterpret_cast<f32x4*>(p + e) = f32x4{acc[e], acc[e + 1], acc[e + 2], acc[e + 3]};
+        if (d0 == 0) {
+            float* ml = part_ml<D>(w, RB, slot, r);
+            ml[0] = m;
+            ml[1] = l;
+        }
+    }
 }
 
-// The parts of a row tile, in part order.
-template <int D, int RB>
-__global__ __launch_bounds__(256) void kv_merge_kernel(KvArgs b, KvOut w, KvCut cut) {
-    KvUnit u;
-    if (!kv_find(b, cut, blockIdx.x, true, &u) || u.parts < 2) return;
-    const int rows = u.q.rows * b.group, row0 = u.tile * RB;
-    constexpr int TPR = D / 4;   // threads a row, four values each
-    for (int r = threadIdx.x / TPR; r < RB && row0 + r < rows; r += 256 / TPR) {
-        const int d0 = (threadIdx.x % TPR) * 4;
-        float m = -INFINITY;
-        for (int p = 0; p < u.parts; ++p) m = fmaxf(m, part_ml<D, RB>(w.part, u.slot + p * b.kv_heads, r)[0]);
-        const float ref = m == -INFINITY ? 0.f : m;
-        float l = 0.f;
-        f32x4 acc{0.f, 0.f, 0.f, 0.f};
-        for (int p = 0; p < u.parts; ++p) {
-            const float* ml = part_ml<D, RB>(w.part, u.slot + p * b.kv_heads, r);
-            const f32x4 v = *reinterpret_cast<const f32x4*>(part_row<D, RB>(w.part, u.slot + p * b.kv_heads, r) + d0);
-            const float f = ml[0] == -INFINITY ? (ml[1] == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(ml[0] - ref);
-            l += f * ml[1];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] += f * v[i];
+// Many query rows.  Workers are workgroups: each of the four waves has 16 of the tile's 64 rows
+// and goes over all the piece's tokens.
+template <int D>
+__global__ __launch_bounds__(256) void kv_prefill_kernel(KvArgs b, const bf16_t* q, int64_t q_stride, KvOut w, float c,
+                                                         KvCut cut) {
+    constexpr int RB = kKvPrefillRows, kStage = KvStage<D>::kBytes;
+    __shared__ __attribute__((aligned(1024))) uint8_t stage0[4 * kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t stage1[4 * kStage];
+    __shared__ KvLine line;
+    kv_line(b, cut, line);
+    const int li = threadIdx.x & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int worker = blockIdx.x;
+    const KvPieces pieces(uniform64(line.before[256]), cut.workers);
+    int64_t pos = pieces.at(min(worker, pieces.workers));
+    const int64_t end = pieces.at(min(worker + 1, pieces.workers));
+    KvMerge entry{-1, 0, 0, 0, 0, 0, 0, 0};
+    KvPlace at;
+    if (pos < end) at.seek(b, cut, line, pos);
+    while (pos < end) {
+        const int h = at.pair % b.kv_heads, tile0 = at.pair / b.kv_heads * RB, rows = at.q.rows * b.group;
+        const int row0 = tile0 + 16 * wave, stop = (int)min((int64_t)at.steps, at.off + (end - pos));
+        if (at.off == 0 && stop < at.steps) {
+            const int last = pieces.holder(pos + at.steps - 1), none = (last + 4) >> 2;
+            entry = KvMerge{last, tile0, min(RB, rows - tile0), at.q.r0, h, none, none, 0};
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        u32x2 o;
-        o[0] = pack_bf16(acc[0] * inv, acc[1] * inv);
-        o[1] = pack_bf16(acc[2] * inv, acc[3] * inv);
-        *reinterpret_cast<u32x2*>(w.out + (int64_t)(u.q.r0 + (row0 + r) / b.group) * w.stride +
-                                  (int64_t)(u.h * b.group + (row0 + r) % b.group) * D + d0) = o;
+        if (row0 < rows) {
+            const int seen = max(0, at.q.len - at.q.rows + 1 + (min(rows, row0 + 16) - 1) / b.group);
+            KvWave<D, 1, false> wv;
+            wv.load_q(b, at.s, at.q, h, q, q_stride, row0);
+            wv.run(b, stage0 + wave * kStage, stage1 + wave * kStage, at.off, min(kv_steps(seen), stop), c);
+            wv.finish();
+            const int slot = 2 * worker + (at.off == 0), rt = 16 * wave + li;
+            if (row0 + li >= rows) {
+            } else if (at.off == 0 && stop == at.steps) {
+                wv.store(out_row<D>(b, w, at.q.r0, h, row0 + li));
+            } else {
+                wv.put_part(part_row<D>(w, RB, slot, rt), part_ml<D>(w, RB, slot, rt));
+            }
+        }
+        pos += stop - at.off;
+        if (pos < end) at.next(b, cut);
+    }
+    if (threadIdx.x == 0) put_merge(w, worker, entry);
+}
+
+// The parts of the cut segments' rows, a row a workgroup at a time: D / 4 threads wide and
+// 1024 / D deep, each depth with its own running maximum over its parts; the order is fixed.
+// Every workgroup looks through the workers for the cut segments and takes its share of them.
+template <int D>
+__global__ __launch_bounds__(256) void kv_merge_kernel(KvArgs b, KvOut w, float c, int rb, int most_rows) {
+    constexpr int TPR = D / 4, PW = 256 / TPR, kMost = kv_workers(D) / 256;
+    __shared__ float sa[PW][D + 4], sm[PW], sl[PW];
+    __shared__ int sums[4], found;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int* last = reinterpret_cast<const int*>(w.ws + (int64_t)w.workers * sizeof(KvMerge));
+    // this thread's workers: kMost of them, bit i of mine: the i-th has a cut segment
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        const int x = threadIdx.x * kMost + i;
+        if (x < w.workers && last[x] >= 0) mine |= 1u << i;
+    }
+    const int n_mine = __popc(mine);
+    int before = (int)wave_scan((int64_t)n_mine);
+    if (lane == 63) sums[wave] = before;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        if (x < wave) before += sums[x];
+        total += sums[x];
+    }
+    before -= n_mine;
+    const int pw = threadIdx.x / TPR, d0 = (threadIdx.x % TPR) * 4;
+    for (int item = blockIdx.x; item < total * most_rows; item += gridDim.x) {
+        int k = item / most_rows - before;
+        if (k >= 0 && k < n_mine) {
+            uint32_t bits = mine;
+            for (; k > 0; --k) bits &= bits - 1;
+            found = threadIdx.x * kMost + __ffs(bits) - 1;
+        }
+        __syncthreads();
+        const int first = __builtin_amdgcn_readfirstlane(found);
+        const KvMerge e = reinterpret_cast<const KvMerge*>(w.ws)[first];
+        const int n0 = min(4 * e.inside0, e.last + 1) - first, n1 = n0 + e.inside1 - e.inside0;
+        const int n = n1 + max(0, e.last + 1 - 4 * e.inside1);
+        for (int r = item % most_rows; r < e.rows; r += most_rows) {
+            float m = -INFINITY, l = 0.f;
+            f32x4 acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+            for (int p = pw; p < n; p += PW) {
+                const int x = p < n0 ? first + p : p < n1 ? 4 * (e.inside0 + p - n0) : 4 * e.inside1 + p - n1;
+                const int slot = 2 * x + (x == first);
+                const float* ml = part_ml<D>(w, rb, slot, r);
+                const f32x4 v = *reinterpret_cast<const f32x4*>(part_row<D>(w, rb, slot, r) + d0);
+                const float mp = ml[0], lp = ml[1], top = fmaxf(m, mp);
+                const float f = part_factor(m, l, top, c), g = part_factor(mp, lp, top, c);
+                m = top;
+                l = l * f + lp * g;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i] = acc[i] * f + v[i] * g;
+            }
+            *reinterpret_cast<f32x4*>(&sa[pw][d0]) = acc;
+            if (d0 == 0) {
+                sm[pw] = m;
+                sl[pw] = l;
+            }
+            __syncthreads();
+            if (pw == 0) {
+                float top = m;
+#pragma unroll
+                for (int p = 1; p < PW; ++p) top = fmaxf(top, sm[p]);
+                l = 0.f;
+                acc = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int p = 0; p < PW; ++p) {
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(&sa[p][d0]);
+                    const float g = part_factor(sm[p], sl[p], top, c);
+                    l += sl[p] * g;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[i] += v[i] * g;
+                }
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                u32x2 o;
+                o[0] = pack2(acc[0] * inv, acc[1] * inv);
+                o[1] = pack2(acc[2] * inv, acc[3] * inv);
+                *reinterpret_cast<u32x2*>(out_row<D>(b, w, e.r0, e.h, e.row0 + r) + d0) = o;
+            }
+            __syncthreads();
+        }
+        __syncthreads();
     }
 }
 
@@ -714,24 +1042,31 @@ template <int D>
 hipError_t attention(const KvArgs& b, const bf16_t* q, int64_t q_stride, bf16_t* out, int64_t out_stride, float scale,
                      int32_t max_rows, void* workspace, hipStream_t s) {
     const float c = scale * 1.44269504088896341f;
-    KvOut w{out, out_stride, static_cast<float*>(workspace)};
-    const int64_t rows = (int64_t)b.n_rows * b.group;
-    auto go = [&](int rb, int cls, auto kern, auto merge) {
-        // tiles, and parts beyond the first of each
-        const int64_t tiles = (rows / rb + b.n_seqs) * b.kv_heads;
-        const KvCut cut{rb, cls, 4};
-        hipLaunchKernelGGL(kern, dim3((unsigned)(tiles + kKvUnits)), dim3(256), 0, s, b, q, q_stride, w, c, cut);
-        // (a sequence of at most min_steps steps is never cut)
-        if (b.max_blocks * kKvBlock > 32 * cut.min_steps)
-            hipLaunchKernelGGL(merge, dim3((unsigned)tiles), dim3(256), 0, s, b, w, cut);
+    const int64_t rows = (int64_t)b.n_rows * b.group, most = (int64_t)max_rows * b.group;
+    auto go = [&](int rb_shift, int cls, int workers, int per_block, auto kern) {
+        // no more workers than steps there can be
+        const int64_t pairs = ((rows >> rb_shift) + b.n_seqs) * b.kv_heads;
+        const int64_t steps = std::max(1, (b.max_blocks + 1) / 2);
+        if (pairs < workers) workers = (int)std::min<int64_t>(workers, pairs * steps);
+        workers = (workers + 3) / 4 * 4;
+        const KvOut w{out, out_stride, static_cast<uint8_t*>(workspace), workers};
+        hipLaunchKernelGGL(kern, dim3(workers / per_block), dim3(256), 0, s, b, q, q_stride, w, c,
+                           KvCut{rb_shift, cls, workers});
+        const int most_rows = (int)std::min<int64_t>(1 << rb_shift, std::max<int64_t>(most, 1));
+        const int grid = (int)std::min<int64_t>(std::min<int64_t>(pairs, workers) * most_rows, 1024);
+        hipLaunchKernelGGL(kv_merge_kernel<D>, dim3(grid), dim3(256), 0, s, b, w, c, 1 << rb_shift, most_rows);
+        return hipGetLastError();
     };
-    if ((int64_t)max_rows * b.group <= kKvRowTile) {
-        go(kKvRowTile, kKvAll, kv_decode_kernel<D>, kv_merge_kernel<D, kKvRowTile>);
-    } else {
-        go(kKvRowTile, kKvFew, kv_decode_kernel<D>, kv_merge_kernel<D, kKvRowTile>);
-        go(kKvPrefillRows, kKvMany, kv_prefill_kernel<D>, kv_merge_kernel<D, kKvPrefillRows>);
-    }
-    return hipGetLastError();
+    static_assert(kKvRowTile == 16 && kKvPrefillRows == 64, "row tiles");
+    // few rows: as many columns of a matrix operation a row as there are
+    const int n = kv_workers(D);
+    if (most <= 1) return go(0, kKvAll, n, 4, kv_decode_kernel<D, 8, true>);
+    if (most <= 2) return go(1, kKvAll, n, 4, kv_decode_kernel<D, 4, true>);
+    if (most <= 4) return go(2, kKvAll, n, 4, kv_decode_kernel<D, 4, false>);
+    if (most <= 8) return go(3, kKvAll, n, 4, kv_decode_kernel<D, 2, false>);
+    if (most <= 16) return go(4, kKvAll, n, 4, kv_decode_kernel<D, 1, false>);
+    hipError_t e = go(4, kKvFew, n, 4, kv_decode_kernel<D, 1, false>);
+    return e != hipSuccess ? e : go(6, kKvMany, n / 4, 1, kv_prefill_kernel<D>);
 }
 
 }  // namespace
