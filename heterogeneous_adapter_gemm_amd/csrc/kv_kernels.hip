@@ -217,13 +217,32 @@ __device__ __forceinline__ int kv_pairs(const KvArgs& b, const KvCut& cut, const
 }
 __device__ __forceinline__ int kv_seg_steps(const KvSeq& q) { return max(1, kv_steps(q.len)); }
 
-// Inclusive sum over the wave's lanes.
+// Inclusive sums over the wave's lanes.
+template <int CTRL, int ROWS_MASK>
+__device__ __forceinline__ int dpp0(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS_MASK, 0xf, ROWS_MASK == 0xf);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+    v += dpp0<0x111, 0xf>(v);   // row_shr 1, 2, 4, 8
+    v += dpp0<0x112, 0xf>(v);
+    v += dpp0<0x114, 0xf>(v);
+    v += dpp0<0x118, 0xf>(v);
+    v += dpp0<0x142, 0xa>(v);   // row_bcast 15, 31
+    v += dpp0<0x143, 0xc>(v);
+    return v;
+}
+template <int CTRL, int ROWS_MASK>
+__device__ __forceinline__ int64_t dpp0(int64_t v) {
+    const uint32_t lo = (uint32_t)dpp0<CTRL, ROWS_MASK>((int)(uint32_t)v);
+    return (int64_t)((uint64_t)lo | (uint64_t)(uint32_t)dpp0<CTRL, ROWS_MASK>((int)(v >> 32)) << 32);
+}
 __device__ __forceinline__ int64_t wave_scan(int64_t v) {
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) {
-        const int64_t o = __shfl_up(v, x, 64);
-        if ((int)(threadIdx.x & 63) >= x) v += o;
-    }
+    v += dpp0<0x111, 0xf>(v);
+    v += dpp0<0x112, 0xf>(v);
+    v += dpp0<0x114, 0xf>(v);
+    v += dpp0<0x118, 0xf>(v);
+    v += dpp0<0x142, 0xa>(v);
+    v += dpp0<0x143, 0xc>(v);
     return v;
 }
 
@@ -438,7 +457,6 @@ struct KvWave {
         h = head;
         s = seq;
         last_block = (sq.len + kKvBlock - 1) / kKvBlock - 1;
-        qsum = 0.f;
         if (r < rows) {
             const bf16_t* p = qp + (int64_t)(sq.r0 + r / b.group) * stride +
                               (int64_t)(h * b.group + r % b.group) * D + lg * (D / 4);
@@ -446,10 +464,7 @@ struct KvWave {
             for (int i = 0; i < W; ++i) {
                 const u32x4 v = ld16(p + 8 * i);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    q[i][j] = v[j];
-                    qsum += bf16_lo(v[j]) + bf16_hi(v[j]);
-                }
+                for (int j = 0; j < 4; ++j) q[i][j] = v[j];
             }
         } else {
 #pragma unroll
@@ -457,7 +472,6 @@ struct KvWave {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) q[i][j] = 0;
         }
-        qsum = sum_lg(qsum);
         const int first = sq.len - sq.rows + 1;   // tokens the sequence's first row sees
         limit = r < rows ? first + r / b.group : 0;
         limit_all = first + row0 / b.group;
@@ -657,6 +671,12 @@ struct KvWave {
         int bad[2];
         bad[0] = load(pg, page_of_word(pg, 0), 0, lds0);
         bad[1] = n > 1 ? load(pg, page_of_word(pg, 1), 1, lds1) : 0;
+        qsum = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) qsum += bf16_lo(q[i][y]) + bf16_hi(q[i][y]);
+        qsum = sum_lg(qsum);
 #pragma unroll 1
         for (int j = 0; j < n; j += 2) {
 #pragma unroll
@@ -949,92 +969,125 @@ __global__ __launch_bounds__(256) void kv_prefill_kernel(KvArgs b, const bf16_t*
     if (threadIdx.x == 0) put_merge(w, worker, entry);
 }
 
-// The parts of the cut segments' rows, a row a workgroup at a time: D / 4 threads wide and
-// 1024 / D deep, each depth with its own running maximum over its parts; the order is fixed.
-// Every workgroup looks through the workers for the cut segments and takes its share of them.
+// Sums of parts at one scale.
+struct KvSum {
+    float m, l;
+    f32x4 acc;
+    __device__ __forceinline__ void add(float mo, float lo, const f32x4& ao, float c) {
+        const float top = fmaxf(m, mo), f = part_factor(m, l, top, c), g = part_factor(mo, lo, top, c);
+        m = top;
+        l = l * f + lo * g;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = acc[i] * f + ao[i] * g;
+    }
+};
+
+// Parts p0, p0 + stride, ... below n of a cut segment's row r, values d0 .. d0 + 3, eight parts'
+// loads at a time.
+template <int D>
+__device__ __forceinline__ KvSum sum_parts(const KvOut& w, const KvMerge& e, int first, int n, int rb, int r, int d0,
+                                           int p0, int stride, float c) {
+    const int n0 = min(4 * e.inside0, e.last + 1) - first, n1 = n0 + e.inside1 - e.inside0;
+    KvSum s{-INFINITY, 0.f, f32x4{0.f, 0.f, 0.f, 0.f}};
+    for (int p = p0; p < n; p += 8 * stride) {
+        f32x4 v[8];
+        float mp[8], lp[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+            const int i = p + y * stride;
+            if (i >= n) continue;
+            const int x = i < n0 ? first + i : i < n1 ? 4 * (e.inside0 + i - n0) : 4 * e.inside1 + i - n1;
+            const int slot = 2 * x + (x == first);
+            const float* ml = part_ml<D>(w, rb, slot, r);
+            v[y] = *reinterpret_cast<const f32x4*>(part_row<D>(w, rb, slot, r) + d0);
+            mp[y] = ml[0];
+            lp[y] = ml[1];
+        }
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+            if (p + y * stride < n) s.add(mp[y], lp[y], v[y], c);
+    }
+    return s;
+}
+
+// The parts of the cut segments' rows, D / 4 threads a row.  Every workgroup looks through the
+// workers for the cut segments and takes its share: a row a wave at a time, or, where there are
+// fewer rows than workgroups, a row a workgroup.  The order of the sums is fixed.
 template <int D>
 __global__ __launch_bounds__(256) void kv_merge_kernel(KvArgs b, KvOut w, float c, int rb, int most_rows) {
-    constexpr int TPR = D / 4, PW = 256 / TPR, kMost = kv_workers(D) / 256;
+    constexpr int TPR = D / 4, PW = 256 / TPR, WW = 64 / TPR, kMost = kv_workers(D) / 256;
     __shared__ float sa[PW][D + 4], sm[PW], sl[PW];
-    __shared__ int sums[4], found;
+    __shared__ int sums[4], list[kv_workers(D)];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int* last = reinterpret_cast<const int*>(w.ws + (int64_t)w.workers * sizeof(KvMerge));
     // this thread's workers: kMost of them, bit i of mine: the i-th has a cut segment
     uint32_t mine = 0;
 #pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-        const int x = threadIdx.x * kMost + i;
-        if (x < w.workers && last[x] >= 0) mine |= 1u << i;
+    for (int i = 0; i < kMost; i += 4) {
+        const int x = threadIdx.x * kMost + i;   // (the workers are a multiple of four)
+        if (x < w.workers) {
+            const u32x4 v = ld16(last + x);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) mine |= (~v[y] >> 31) << (i + y);
+        }
     }
-    const int n_mine = __popc(mine);
-    int before = (int)wave_scan((int64_t)n_mine);
-    if (lane == 63) sums[wave] = before;
+    int at = wave_scan((int)__popc(mine));
+    if (lane == 63) sums[wave] = at;
     __syncthreads();
     int total = 0;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-        if (x < wave) before += sums[x];
+        if (x < wave) at += sums[x];
         total += sums[x];
     }
-    before -= n_mine;
-    const int pw = threadIdx.x / TPR, d0 = (threadIdx.x % TPR) * 4;
-    for (int item = blockIdx.x; item < total * most_rows; item += gridDim.x) {
-        int k = item / most_rows - before;
-        if (k >= 0 && k < n_mine) {
-            uint32_t bits = mine;
-            for (; k > 0; --k) bits &= bits - 1;
-            found = threadIdx.x * kMost + __ffs(bits) - 1;
-        }
-        __syncthreads();
-        const int first = __builtin_amdgcn_readfirstlane(found);
+    at -= __popc(mine);
+    for (; mine; mine &= mine - 1) list[at++] = threadIdx.x * kMost + __ffs(mine) - 1;
+    __syncthreads();
+    const int items = total * most_rows;
+    const bool per_wave = items > (int)gridDim.x;
+    auto store = [&](const KvMerge& e, int r, int d0, const KvSum& s) {
+        const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
+        u32x2 o;
+        o[0] = pack2(s.acc[0] * inv, s.acc[1] * inv);
+        o[1] = pack2(s.acc[2] * inv, s.acc[3] * inv);
+        *reinterpret_cast<u32x2*>(out_row<D>(b, w, e.r0, e.h, e.row0 + r) + d0) = o;
+    };
+    const int d0 = threadIdx.x % TPR * 4;
+    for (int item = per_wave ? 4 * blockIdx.x + wave : blockIdx.x; item < items; item += (per_wave ? 4 : 1) * gridDim.x) {
+        const int first = __builtin_amdgcn_readfirstlane(list[item / most_rows]);
         const KvMerge e = reinterpret_cast<const KvMerge*>(w.ws)[first];
-        const int n0 = min(4 * e.inside0, e.last + 1) - first, n1 = n0 + e.inside1 - e.inside0;
-        const int n = n1 + max(0, e.last + 1 - 4 * e.inside1);
+        const int n0 = min(4 * e.inside0, e.last + 1) - first + e.inside1 - e.inside0;
+        const int n = n0 + max(0, e.last + 1 - 4 * e.inside1);
+        // (most_rows is only what the caller expects)
         for (int r = item % most_rows; r < e.rows; r += most_rows) {
-            float m = -INFINITY, l = 0.f;
-            f32x4 acc{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-            for (int p = pw; p < n; p += PW) {
-                const int x = p < n0 ? first + p : p < n1 ? 4 * (e.inside0 + p - n0) : 4 * e.inside1 + p - n1;
-                const int slot = 2 * x + (x == first);
-                const float* ml = part_ml<D>(w, rb, slot, r);
-                const f32x4 v = *reinterpret_cast<const f32x4*>(part_row<D>(w, rb, slot, r) + d0);
-                const float mp = ml[0], lp = ml[1], top = fmaxf(m, mp);
-                const float f = part_factor(m, l, top, c), g = part_factor(mp, lp, top, c);
-                m = top;
-                l = l * f + lp * g;
+            if (per_wave) {
+                KvSum s = sum_parts<D>(w, e, first, n, rb, r, d0, lane / TPR, WW, c);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[i] = acc[i] * f + v[i] * g;
+                for (int x = TPR; x < 64; x <<= 1) {
+                    f32x4 o;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = __shfl_xor(s.acc[i], x, 64);
+                    const float mo = __shfl_xor(s.m, x, 64), lo = __shfl_xor(s.l, x, 64);
+                    s.add(mo, lo, o, c);
+                }
+                if (lane < TPR) store(e, r, d0, s);
+                continue;
             }
-            *reinterpret_cast<f32x4*>(&sa[pw][d0]) = acc;
+            const int pw = threadIdx.x / TPR;
+            KvSum s = sum_parts<D>(w, e, first, n, rb, r, d0, pw, PW, c);
+            *reinterpret_cast<f32x4*>(&sa[pw][d0]) = s.acc;
             if (d0 == 0) {
-                sm[pw] = m;
-                sl[pw] = l;
+                sm[pw] = s.m;
+                sl[pw] = s.l;
             }
             __syncthreads();
             if (pw == 0) {
-                float top = m;
 #pragma unroll
-                for (int p = 1; p < PW; ++p) top = fmaxf(top, sm[p]);
-                l = 0.f;
-                acc = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int p = 0; p < PW; ++p) {
-                    const f32x4 v = *reinterpret_cast<const f32x4*>(&sa[p][d0]);
-                    const float g = part_factor(sm[p], sl[p], top, c);
-                    l += sl[p] * g;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[i] += v[i] * g;
-                }
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                u32x2 o;
-                o[0] = pack2(acc[0] * inv, acc[1] * inv);
-                o[1] = pack2(acc[2] * inv, acc[3] * inv);
-                *reinterpret_cast<u32x2*>(out_row<D>(b, w, e.r0, e.h, e.row0 + r) + d0) = o;
+                for (int x = 1; x < PW; ++x) s.add(sm[x], sl[x], *reinterpret_cast<const f32x4*>(&sa[x][d0]), c);
+                store(e, r, d0, s);
             }
             __syncthreads();
         }
-        __syncthreads();
     }
 }
 
