@@ -93,6 +93,19 @@ __device__ __forceinline__ int xcd_logical(int bid, int total) {
     return xcd < rr ? xcd * (q + 1) + idx : rr * (q + 1) + (xcd - rr) * q + idx;
 }
 
+// After a wait for direct loads into LDS: no read of LDS moves before it, no load after it.
+__device__ __forceinline__ void landed() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// s_waitcnt lgkmcnt(0), the other counters unconstrained, and nothing moved over it
+__device__ __forceinline__ void wait_lgkm0() {
+    landed();
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    landed();
+}
+
 typedef __attribute__((address_space(3))) void* lds_vptr;
 
 // buffer resource word 3 for raw (unformatted, unswizzled) 32-bit access on CDNA
@@ -124,6 +137,11 @@ __device__ __forceinline__ void buffer_load_lds16(const void* base, int bytes, v
 // 16 bytes per lane straight into LDS (lane i -> lds + 16 i) from a per-lane global address
 __device__ __forceinline__ void global_load_lds16(const void* p, void* lds) {
     __builtin_amdgcn_global_load_lds(const_cast<void*>(p), (lds_vptr)lds, 16, 0, 0);
+}
+
+// 4 bytes per lane straight into LDS (lane i -> lds + 4 i) from a per-lane global address
+__device__ __forceinline__ void global_load_lds4(const void* p, void* lds) {
+    __builtin_amdgcn_global_load_lds(const_cast<void*>(p), (lds_vptr)lds, 4, 0, 0);
 }
 
 __device__ __forceinline__ float wave_sum(float v) {

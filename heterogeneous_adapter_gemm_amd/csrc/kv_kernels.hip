@@ -378,14 +378,6 @@ __device__ __forceinline__ float sum_lg(float v) {
     return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
-// 4 bytes per lane straight into LDS (lane i -> lds + 4 i)
-__device__ __forceinline__ void global_load_lds4(const void* p, void* lds) {
-    __builtin_amdgcn_global_load_lds(const_cast<void*>(p), (lds_vptr)lds, 4, 0, 0);
-}
-
-// s_waitcnt lgkmcnt(0), the other counters unconstrained
-__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
-
 // A wave's place for one step in LDS: the codes of two slabs of keys and two of values, then
 // their words.
 template <int D>
@@ -685,6 +677,7 @@ struct KvWave {
                 // this step's loads have landed (of the ones after them, the next step's alone are out)
                 if (j + x + 1 < n) wait_vmcnt<kLoads>();
                 else wait_vmcnt<0>();
+                landed();
                 uint32_t kc[2][W], vc[2][W], kw[NEL], vw[NEL];
                 read(x ? lds1 : lds0, kc, vc, kw, vw);
                 const int bad_now = bad[x];

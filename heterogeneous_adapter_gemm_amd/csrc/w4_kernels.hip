@@ -5,132 +5,428 @@
 //
 // The matrix cores run bf16 on the codes themselves: a nibble put in the top
 // four bits of bf16's mantissa stands for 16 + code exactly, so a code needs a
-// shift and one and-or, and no rounding.  Per group, fp32: y += scale * (acc -
-// (16 + zero) * sum(x)), the sum of x from one more matrix operation against
-// ones.
+// shift and one and-or, and no rounding.  Per group, fp32: y += scale * acc -
+// scale * (16 + zero) * sum(x): the second term is one fp32 matrix operation of
+// each lane's own sum of its x.
+//
+// A lane of a matrix operation has a row of x (a row of codes) and its share of
+// a group's k, consecutive ones: group / 4 of them where four lanes share a row
+// (16-row operations), group / 2 where two do (32-row operations).
 #include "common.h"
 #include "internal.h"
 
 namespace hagemm {
 namespace {
 
-// (16 + nibble k, 16 + nibble k + 4) of w as two bf16
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int k) {
-    const uint32_t s = k == 0 ? w << 3 : k == 1 ? w >> 1 : k == 2 ? w >> 5 : w >> 9;
-    return (s & 0x00780078u) | 0x41804180u;
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// (16 + nibble k, 16 + nibble k + 4) of w as two bf16; the constants in registers (a
+// three-operand and-or takes none of its own)
+struct CodeConst {
+    uint32_t mask = 0x00780078u, ones = 0x41804180u;
+    __device__ __forceinline__ CodeConst() { asm volatile("" : "+v"(mask), "+v"(ones)); }
+};
+__device__ __forceinline__ u32x4 code_values(const CodeConst& c, uint32_t w) {
+    return u32x4{((w << 3) & c.mask) | c.ones, ((w >> 1) & c.mask) | c.ones, ((w >> 5) & c.mask) | c.ones,
+                 ((w >> 9) & c.mask) | c.ones};
 }
 
-// eight consecutive x in the order of code_pair's elements: 0, 4, 1, 5, 2, 6, 3, 7
+// eight consecutive x in the order of code_values' elements: 0, 4, 1, 5, 2, 6, 3, 7
 __device__ __forceinline__ u32x4 code_order(const u32x4& v) {
     return u32x4{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
                  __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
 }
 
+// s plus the eight x of v
+__device__ __forceinline__ float add_x(const u32x4& v, float s) {
+    const bf16x2 one = __builtin_bit_cast(bf16x2, 0x3F803F80u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = v[i];   // (a bit cast of v[i] itself reads v[0])
+        s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), one, s, false);
+    }
+    return s;
+}
+
+__device__ __forceinline__ f32x16 mma32(const u32x4& a, const u32x4& b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
+}
+
 __device__ __forceinline__ float half_lo(uint32_t w) { return (float)__builtin_bit_cast(_Float16, (uint16_t)w); }
 __device__ __forceinline__ float half_hi(uint32_t w) { return (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16)); }
 
-constexpr int kW4Waves = 4;
-
-// One workgroup per 16 columns of y and 16 MB rows: its waves take the 128-deep pieces of K in
-// turn, and their sums meet in LDS in wave order.
-template <int MB, int G>
-__global__ __launch_bounds__(64 * kW4Waves) void gemm_w4_kernel(const bf16_t* __restrict__ x,
-                                                                const uint8_t* __restrict__ q,
-                                                                const uint32_t* __restrict__ sz, bf16_t* __restrict__ y,
-                                                                int M, int N, int K, const int32_t* __restrict__ row_slot,
-                                                                float* __restrict__ ybase) {
-    __shared__ float part[kW4Waves][MB][4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, lg = lane >> 4;
-    const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MB;
-    const int n = min(n0 + li, N - 1);
-    constexpr int NG = 128 / G;
-    const uint8_t* qn = q + (int64_t)n * (K / 2);
-    const uint32_t* sn = sz + (int64_t)n * (K / G);
-    // k of this lane's eight codes of step s: one 16-byte load a lane where a group is 128 deep
-    const int kl = G == 128 ? lg * 32 : lg * 8, ks = G == 128 ? 8 : 32;
-    f32x4 acc[MB];
+template <int W>
+__device__ __forceinline__ void ld_words(const uint8_t* p, uint32_t (&o)[W]) {
+    if constexpr (W == 1) {
+        o[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (W == 2) {
+        const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+        o[0] = v[0];
+        o[1] = v[1];
+    } else {
 #pragma unroll
-    for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const u32x4 ones{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-    struct Piece {
-        uint32_t c[4], s[NG];
-    };
-    auto load = [&](int kb, Piece& p) {
-        if constexpr (G == 128) {
-            const u32x4 v = ld16(qn + kb / 2 + lg * 16);
+        for (int j = 0; j < W / 4; ++j) {
+            const u32x4 v = ld16(p + 16 * j);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p.c[i] = v[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p.c[i] = *reinterpret_cast<const uint32_t*>(qn + kb / 2 + i * 16 + lg * 4);
+            for (int i = 0; i < 4; ++i) o[4 * j + i] = v[i];
         }
-#pragma unroll
-        for (int g = 0; g < NG; ++g) p.s[g] = sn[kb / G + g];
+    }
+}
+
+__device__ __forceinline__ void put(bf16_t* y, float* ybase, const int32_t* row_slot, int m, int n, int N, float v) {
+    const int64_t off = (int64_t)m * N + n;
+    if (row_slot != nullptr && row_slot[m] >= 0)
+        ybase[off] = v;
+    else
+        y[off].bits = (uint16_t)f32_to_bf16(v);
+}
+
+// ---------------------------------------------------------------- up to 16 rows
+
+// One workgroup per 16 columns of y: its eight waves take the 128-deep pieces of K in turn (the
+// codes of the next three in flight, x of the next one), and their sums meet in LDS in wave
+// order.  Bound by reading the codes once; at a few microseconds, by the latency of that.
+constexpr int kRowWaves = 8;
+
+template <int G>
+__global__ __launch_bounds__(64 * kRowWaves) void gemm_w4_rows_kernel(
+    const bf16_t* __restrict__ x, const uint8_t* __restrict__ q, const uint32_t* __restrict__ sz,
+    bf16_t* __restrict__ y, int M, int N, int K, const int32_t* __restrict__ row_slot, float* __restrict__ ybase) {
+    __shared__ float part[kRowWaves][4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, lg = lane >> 4;
+    const int n0 = blockIdx.x * 16, n = min(n0 + li, N - 1);
+    constexpr int NG = 128 / G, W = G / 32;   // groups of a piece; words (and steps) of a group a lane
+    const uint8_t* qn = q + (int64_t)n * (K / 2) + lg * (G / 8);
+    const uint32_t* sn = sz + (int64_t)n * (K / G);
+    const bf16_t* xm = x + (int64_t)min(li, M - 1) * K + lg * (G / 4);
+    const bool row = li < M;
+    const CodeConst cc;
+    struct Codes {
+        uint32_t c[NG][W], s[NG];
     };
-    auto mul = [&](int kb, const Piece& p) {
+    struct Rows {
+        u32x4 x[NG][W];
+    };
+    auto load = [&](int kb, Codes& p) {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            const float sc = half_lo(p.s[g]), zr = 16.f + half_hi(p.s[g]);
-            f32x4 d[MB], xs[MB];
+            ld_words(qn + (kb + g * G) / 2, p.c[g]);
+            p.s[g] = sn[kb / G + g];
+        }
+    };
+    auto load_x = [&](int kb, Rows& p) {
 #pragma unroll
-            for (int b = 0; b < MB; ++b) d[b] = xs[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int g = 0; g < NG; ++g)
 #pragma unroll
-            for (int t = 0; t < G / 32; ++t) {
-                const int s = g * (G / 32) + t;
-                u32x4 cf;
+            for (int t = 0; t < W; ++t) {
+                p.x[g][t] = u32x4{0, 0, 0, 0};
+                if (row) p.x[g][t] = ld16(xm + kb + g * G + 8 * t);
+            }
+    };
+    f32x4 acc{0.f, 0.f, 0.f, 0.f};
+    constexpr int PF = 4, kStep = 128 * kRowWaves;
+    Codes p[PF];
+    Rows r[2];
+    const int k0 = wave * 128, last = K - 128;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) cf[i] = code_pair(p.c[s], i);
+    for (int i = 0; i < PF; ++i) load(min(k0 + i * kStep, last), p[i]);
+    load_x(min(k0, last), r[0]);
+    for (int kb0 = k0; kb0 < K; kb0 += PF * kStep) {
 #pragma unroll
-                for (int b = 0; b < MB; ++b) {
-                    const int m = m0 + 16 * b + li;
-                    u32x4 xf{0, 0, 0, 0};
-                    if (m < M) xf = code_order(ld16(x + (int64_t)m * K + kb + kl + s * ks));
-                    d[b] = mma_step(xf, cf, d[b], bf16_t{});
-                    xs[b] = mma_step(xf, ones, xs[b], bf16_t{});
+        for (int i = 0; i < PF; ++i) {
+            const int kb = kb0 + i * kStep;
+            if (kb >= K) break;
+            const Codes now = p[i];
+            load_x(min(kb + kStep, last), r[(i + 1) & 1]);
+            load(min(kb + PF * kStep, last), p[i]);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float sc = half_lo(now.s[g]), corr = -sc * (16.f + half_hi(now.s[g]));
+                f32x4 d{0.f, 0.f, 0.f, 0.f};
+                float xs = 0.f;
+#pragma unroll
+                for (int t = 0; t < W; ++t) {
+                    const u32x4 v = r[i & 1].x[g][t];
+                    d = mma_step(code_order(v), code_values(cc, now.c[g][t]), d, bf16_t{});
+                    xs = add_x(v, xs);
+                }
+                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(xs, corr, acc, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[j] = fmaf(sc, d[j], acc[j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    if (wave < 4) {
+        // wave i: rows 4 lg + i
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRowWaves; ++w) v += part[w][wave][lane];
+        const int m = 4 * lg + wave;
+        if (m < M && n0 + li < N) put(y, ybase, row_slot, m, n0 + li, N, v);
+    }
+}
+
+// ---------------------------------------------------------------- 32-row operations
+
+// Codes and scales of a piece of 32 NB columns, in LDS: 2 KB of codes a block of 32 columns, a
+// lane's own 16 bytes (two of them) in a row, then the scales and zeros of a group, a word a lane.
+template <int G, int NB>
+struct W4Cols {
+    static constexpr int NG = 128 / G, S = G / 16;   // groups of a piece; steps (words a lane) of a group
+    static constexpr int kBytes = NB * 2048 + NG * 256;
+    struct Codes {
+        uint32_t c[NB][NG][S], s[NB][NG];
+    };
+    const uint8_t* qn[NB];
+    const uint32_t *sn, *sb[NB];   // scales: a lane's of all the blocks' columns; of its column of each block
+
+    __device__ __forceinline__ W4Cols(const uint8_t* q, const uint32_t* sz, int n0, int N, int K) {
+        const int lane = threadIdx.x & 63, lr = lane & 31, hg = lane >> 5;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+        {
+            const int64_t n = min(n0 + 32 * b + lr, N - 1);
+            qn[b] = q + n * (K / 2) + hg * (G == 128 ? 32 : 16);
+            sb[b] = sz + n * (K / G);
+        }
+        sn = sz + (int64_t)min(n0 + (NB == 2 ? lane : lr), N - 1) * (K / G);
+    }
+    // straight to registers
+    __device__ __forceinline__ void load(int kb, Codes& p) const {
+        const int hg = (threadIdx.x & 63) >> 5;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                ld_words(qn[b] - hg * (G == 128 ? 32 : 16) + (kb + g * G) / 2 + hg * (G / 4), p.c[b][g]);
+                p.s[b][g] = sb[b][kb / G + g];
+            }
+    }
+    __device__ __forceinline__ void load(int kb, uint8_t* to) const {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                global_load_lds16(qn[b] + kb / 2 + i * (G == 128 ? 16 : 32), to + (2 * b + i) * 1024);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) global_load_lds4(sn + kb / G + g, to + NB * 2048 + g * 256);
+    }
+    __device__ __forceinline__ void read(const uint8_t* from, Codes& p) const {
+        const int lane = threadIdx.x & 63, lr = lane & 31, hg = lane >> 5;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if constexpr (G == 32) {
+                    // a lane's 16 bytes are one group of its column: it wants half of both
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        ld_words(from + (2 * b + i) * 1024 + (32 * u + lr) * 16 + hg * 8, p.c[b][2 * i + u]);
+                } else {
+                    const u32x4 v = ld16(from + (2 * b + i) * 1024 + lane * 16);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) p.c[b][G == 128 ? 0 : i][G == 128 ? 4 * i + y : y] = v[y];
                 }
             }
 #pragma unroll
-            for (int b = 0; b < MB; ++b)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[b][i] += sc * (d[b][i] - zr * xs[b][i]);
+            for (int g = 0; g < NG; ++g)
+                p.s[b][g] = *reinterpret_cast<const uint32_t*>(from + NB * 2048 + g * 256 + (32 * b + lr) * 4);
         }
-    };
-    constexpr int PF = 4;
-    Piece p[PF];
-    const int step = 128 * kW4Waves;
+    }
+};
+
+// x rows in LDS: [row][16 chunks of 16 bytes], chunk i of row r in slot i ^ (r % 16), so that the
+// rows of a read differ in their banks.  A wave-load fills four rows.
+__device__ __forceinline__ void load_rows(const bf16_t* x, int m0, int M, int K, int kb, uint8_t* lds, int first, int count) {
+    const int lane = threadIdx.x & 63;
+    for (int i = 0; i < count; ++i) {
+        const int r = first + 4 * i + (lane >> 4), slot = lane & 15;
+        const int m = min(m0 + r, M - 1);
+        global_load_lds16(x + (int64_t)m * K + kb + (slot ^ (r & 15)) * 8, lds + (first + 4 * i) * 256);
+    }
+}
+
+// One 128-deep piece: acc[a][b] += rows 32 a of x (LDS at xs, first row r0) times columns 32 b.
+template <int G, int MB, int NB>
+__device__ __forceinline__ void mul_piece(const uint8_t* xs, int r0, const typename W4Cols<G, NB>::Codes& p,
+                                          const CodeConst& cc, f32x16 (&acc)[MB][NB]) {
+    constexpr int NG = 128 / G, S = G / 16;
+    const int lr = threadIdx.x & 31, hg = (threadIdx.x & 63) >> 5;
 #pragma unroll
-    for (int i = 0; i < PF; ++i) load(min(wave * 128 + i * step, K - 128), p[i]);
-    for (int k0 = wave * 128; k0 < K; k0 += PF * step) {
+    for (int g = 0; g < NG; ++g) {
+        f32x16 d[MB][NB];
+        float sum[MB];
 #pragma unroll
-        for (int i = 0; i < PF; ++i) {
-            const int kb = k0 + i * step;
-            if (kb < K) {
-                const Piece now = p[i];
-                load(min(kb + PF * step, K - 128), p[i]);
-                mul(kb, now);
+        for (int a = 0; a < MB; ++a) {
+            sum[a] = 0.f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) d[a][b][i] = 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < S; ++t) {
+            u32x4 cf[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) cf[b] = code_values(cc, p.c[b][g][t]);
+#pragma unroll
+            for (int a = 0; a < MB; ++a) {
+                const int r = r0 + 32 * a + lr;
+                const u32x4 v = ld16(xs + r * 256 + ((g * (G / 8) + hg * S + t) ^ (r & 15)) * 16);
+                sum[a] = add_x(v, sum[a]);
+                const u32x4 xf = code_order(v);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) d[a][b] = mma32(xf, cf[b], d[a][b]);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const float sc = half_lo(p.s[b][g]), corr = -sc * (16.f + half_hi(p.s[b][g]));
+#pragma unroll
+            for (int a = 0; a < MB; ++a) {
+                acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(sum[a], corr, acc[a][b], 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[a][b][i] = fmaf(sc, d[a][b][i], acc[a][b][i]);
             }
         }
     }
+}
+
+// Row of register i of a 32 x 32 block
+__device__ __forceinline__ int row32(int i) { return 8 * (i / 4) + 4 * ((threadIdx.x & 63) >> 5) + i % 4; }
+
+// Decode batches: 32 MB rows by 32 NB columns a workgroup, its four waves taking the 128-deep
+// pieces of K in turn, each with its own place for x in LDS (two pieces, the next one in flight)
+// and no barrier until their sums meet there.
+template <int G, int MB, int NB>
+__global__ __launch_bounds__(256) void gemm_w4_decode_kernel(const bf16_t* __restrict__ x, const uint8_t* __restrict__ q,
+                                                             const uint32_t* __restrict__ sz, bf16_t* __restrict__ y, int M,
+                                                             int N, int K, const int32_t* __restrict__ row_slot,
+                                                             float* __restrict__ ybase) {
+    using Cols = W4Cols<G, NB>;
+    constexpr int kRows = 32 * MB, kStage = kRows * 256;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds0[4 * kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds1[4 * kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t ldsc[4 * Cols::kBytes];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = blockIdx.x * 32 * NB, m0 = blockIdx.y * kRows;
+    const Cols cols(q, sz, n0, N, K);
+    const CodeConst cc;
+    uint8_t* st0 = lds0 + wave * kStage;
+    uint8_t* st1 = lds1 + wave * kStage;
+    uint8_t* stc = ldsc + wave * Cols::kBytes;
+    f32x16 acc[MB][NB];
 #pragma unroll
-    for (int b = 0; b < MB; ++b)
+    for (int a = 0; a < MB; ++a)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part[wave][b][i][lane] = acc[b][i];
-    __syncthreads();
-    for (int b = wave; b < MB; b += kW4Waves) {
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float v = 0.f;
+            for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
+    const int n = (K / 128 - wave + 3) / 4;   // pieces of this wave
+    auto issue = [&](int j, uint8_t* to) {
+        const int kb = (wave + 4 * j) * 128;
+        load_rows(x, m0, M, K, kb, to, 0, kRows / 4);
+        cols.load(kb, stc);
+    };
+    if (n > 0) issue(0, st0);
+#pragma unroll 1
+    for (int j = 0; j < n; j += 2) {
 #pragma unroll
-            for (int w = 0; w < kW4Waves; ++w) v += part[w][b][i][lane];
-            const int m = m0 + 16 * b + 4 * lg + i;
-            if (m >= M || n0 + li >= N) continue;
-            const int64_t off = (int64_t)m * N + n0 + li;
-            if (row_slot != nullptr && row_slot[m] >= 0)
-                ybase[off] = v;
-            else
-                y[off].bits = (uint16_t)f32_to_bf16(v);
+        for (int u = 0; u < 2; ++u) {
+            if (j + u >= n) break;
+            wait_vmcnt<0>();
+            landed();
+            typename Cols::Codes p;
+            cols.read(stc, p);
+            // the codes are in registers and the other place has been used up: the next piece goes there
+            wait_lgkm0();
+            if (j + u + 1 < n) issue(j + u + 1, u ? st0 : st1);
+            mul_piece<G, MB, NB>(u ? st1 : st0, 0, p, cc, acc);
         }
     }
+    // the waves' sums, 16 registers of a block at a time: [wave][i][lane]
+    float* part = reinterpret_cast<float*>(lds0);
+    static_assert(4 * kStage >= 4 * 16 * 64 * 4, "a block's sums fit");
+#pragma unroll
+    for (int a = 0; a < MB; ++a)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) part[(wave * 16 + i) * 64 + lane] = acc[a][b][i];
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int reg = 4 * wave + i;
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) v += part[(w * 16 + reg) * 64 + lane];
+                const int m = m0 + 32 * a + row32(reg), c = n0 + 32 * b + (lane & 31);
+                if (m < M && c < N) put(y, ybase, row_slot, m, c, N, v);
+            }
+        }
+}
+
+// Long batches: 128 x 128 of y a workgroup, 64 x 64 a wave; the 128-deep pieces of x go to LDS
+// once for the four waves, one piece ahead.  Bound by the matrix cores and, about as much, by
+// putting the codes in place and the sums of a group to scale.
+template <int G>
+__global__ __launch_bounds__(256, 2) void gemm_w4_long_kernel(const bf16_t* __restrict__ x, const uint8_t* __restrict__ q,
+                                                              const uint32_t* __restrict__ sz, bf16_t* __restrict__ y,
+                                                              int M, int N, int K, const int32_t* __restrict__ row_slot,
+                                                              float* __restrict__ ybase) {
+    using Cols = W4Cols<G, 2>;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds0[128 * 256];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds1[128 * 256];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int row_blocks = (M + 127) / 128;
+    const int lid = xcd_logical(blockIdx.x, gridDim.x);
+    const int m0 = (lid % row_blocks) * 128, n0 = (lid / row_blocks) * 128 + (wave & 1) * 64;
+    const int r0 = (wave >> 1) * 64;
+    const Cols cols(q, sz, n0, N, K);
+    const CodeConst cc;
+    f32x16 acc[2][2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
+    const int n = K / 128;
+    typename Cols::Codes p[2];
+    auto issue = [&](int j, uint8_t* to, typename Cols::Codes& c) {
+        load_rows(x, m0, M, K, j * 128, to, 32 * wave, 8);
+        cols.load(j * 128, c);
+    };
+    issue(0, lds0, p[0]);
+#pragma unroll 1
+    for (int j = 0; j < n; j += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (j + u >= n) break;
+            wait_vmcnt<0>();
+            landed();
+            __builtin_amdgcn_s_barrier();   // every wave's rows are there, and the other place is read
+            landed();
+            if (j + u + 1 < n) issue(j + u + 1, u ? lds0 : lds1, p[1 - u]);
+            mul_piece<G, 2, 2>(u ? lds1 : lds0, r0, p[u], cc, acc);
+        }
+    }
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int m = m0 + r0 + 32 * a + row32(i), c = n0 + 32 * b + (threadIdx.x & 31);
+                if (m < M && c < N) put(y, ybase, row_slot, m, c, N, acc[a][b][i]);
+            }
 }
 
 }  // namespace
@@ -141,24 +437,33 @@ bool gemm_w4_ok(int64_t M, int64_t N, int64_t K, int32_t group) {
     return M * K * 2 < INT32_MAX && N * K / 2 < INT32_MAX;
 }
 
-hipError_t launch_gemm_w4(const void* x, const void* q, const void* sz, int32_t group, void* y, int64_t M64, int64_t N64,
-                          int64_t K64, const int32_t* row_slot, float* ybase, hipStream_t s) {
-    if (!gemm_w4_ok(M64, N64, K64, group)) return hipErrorInvalidValue;
-    const int M = (int)M64, N = (int)N64, K = (int)K64;
-    auto go = [&](auto kern, int bm) {
-        hipLaunchKernelGGL(kern, dim3((N + 15) / 16, (M + bm - 1) / bm), dim3(64 * kW4Waves), 0, s,
-                           static_cast<const bf16_t*>(x), static_cast<const uint8_t*>(q),
-                           static_cast<const uint32_t*>(sz), static_cast<bf16_t*>(y), M, N, K, row_slot, ybase);
+template <int G>
+static hipError_t gemm_w4(const bf16_t* x, const uint8_t* q, const uint32_t* sz, bf16_t* y, int M, int N, int K,
+                          const int32_t* row_slot, float* ybase, hipStream_t s) {
+    auto go = [&](auto kern, int64_t gx, int64_t gy, int threads) {
+        if (gx > INT32_MAX || gy > 65535) return hipErrorInvalidValue;
+        hipLaunchKernelGGL(kern, dim3((unsigned)gx, (unsigned)gy), dim3(threads), 0, s, x, q, sz, y, M, N, K, row_slot, ybase);
+        return hipGetLastError();
     };
-    auto by_rows = [&](auto k1, auto k2, auto k4) {
-        if (M <= 16) go(k1, 16);
-        else if (M <= 32) go(k2, 32);
-        else go(k4, 64);
-    };
-    if (group == 128) by_rows(gemm_w4_kernel<1, 128>, gemm_w4_kernel<2, 128>, gemm_w4_kernel<4, 128>);
-    else if (group == 64) by_rows(gemm_w4_kernel<1, 64>, gemm_w4_kernel<2, 64>, gemm_w4_kernel<4, 64>);
-    else by_rows(gemm_w4_kernel<1, 32>, gemm_w4_kernel<2, 32>, gemm_w4_kernel<4, 32>);
-    return hipGetLastError();
+    auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    if (M <= 16) return go(gemm_w4_rows_kernel<G>, cdiv(N, 16), 1, 64 * kRowWaves);
+    const int64_t tiles = cdiv(M, 128) * cdiv(N, 128);
+    if (M > 64 && tiles >= 128) return go(gemm_w4_long_kernel<G>, tiles, 1, 256);
+    if (M <= 32) return go(gemm_w4_decode_kernel<G, 1, 1>, cdiv(N, 32), 1, 256);
+    if (N >= 64 * 160) return go(gemm_w4_decode_kernel<G, 2, 2>, cdiv(N, 64), cdiv(M, 64), 256);
+    return go(gemm_w4_decode_kernel<G, 2, 1>, cdiv(N, 32), cdiv(M, 64), 256);
+}
+
+hipError_t launch_gemm_w4(const void* x, const void* q, const void* sz, int32_t group, void* y, int64_t M, int64_t N,
+                          int64_t K, const int32_t* row_slot, float* ybase, hipStream_t s) {
+    if (!gemm_w4_ok(M, N, K, group)) return hipErrorInvalidValue;
+    const bf16_t* xb = static_cast<const bf16_t*>(x);
+    const uint8_t* qb = static_cast<const uint8_t*>(q);
+    const uint32_t* zb = static_cast<const uint32_t*>(sz);
+    bf16_t* yb = static_cast<bf16_t*>(y);
+    if (group == 128) return gemm_w4<128>(xb, qb, zb, yb, (int)M, (int)N, (int)K, row_slot, ybase, s);
+    if (group == 64) return gemm_w4<64>(xb, qb, zb, yb, (int)M, (int)N, (int)K, row_slot, ybase, s);
+    return gemm_w4<32>(xb, qb, zb, yb, (int)M, (int)N, (int)K, row_slot, ybase, s);
 }
 
 }  // namespace hagemm

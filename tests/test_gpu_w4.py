@@ -52,7 +52,8 @@ def product_tolerance(want, x, scale, zero, K):
 
 SHAPES = [(1, 16, 128, 128), (1, 4096, 4096, 128), (3, 20, 256, 32), (16, 528, 1152, 64), (17, 4, 128, 32), (31, 260, 512, 128),
           (33, 1000, 640, 64), (64, 4096, 1024, 128), (65, 1004, 384, 32), (130, 516, 768, 128), (300, 272, 640, 64),
-          (520, 1040, 256, 32)]
+          (520, 1040, 256, 32), (48, 10244, 256, 128), (70, 10260, 384, 64), (40, 10240, 128, 32), (520, 4100, 384, 128),
+          (1100, 2052, 256, 64), (129, 16388, 128, 32)]
 
 
 @pytest.mark.parametrize("M,N,K,group", SHAPES)
