@@ -378,6 +378,22 @@ __device__ __forceinline__ float sum_lg(float v) {
     return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
+// Over the two lanes that share a query row (lane % 32).
+__device__ __forceinline__ float max_hg(float v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float sum_hg(float v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+__device__ __forceinline__ f32x16_t mma32(const u32x4& a, const u32x4& b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
+}
+
 // A wave's place for one step in LDS: the codes of two slabs of keys and two of values, then
 // their words.
 template <int D>
@@ -916,17 +932,235 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 3) void kv_decode_kernel(KvArgs
     }
 }
 
-// Many query rows.  Workers are workgroups: each of the four waves has 16 of the tile's 64 rows
-// and goes over all the piece's tokens.
+// ---------------------------------------------------------------- attention: many query rows
+
+// Workers are workgroups: the four waves have 32 of a tile's 128 rows each and share the tokens'
+// slabs, 64 tokens a stage, wave w bringing block w straight to LDS one stage ahead.  Codes are
+// put in place by every wave for itself.  Bound by the vector units: the softmax's exponentials
+// and sums, then the codes.
+//
+// 32-row matrix operations: lane (r, hg) = (lane % 32, lane / 32) holds everything of query row r:
+// of 32 tokens' scores those of tokens 8 x + 4 hg .. + 3 (x 0..3), of the output as store() says.
+// The weights are rounded to bf16 once here (half a step is 2^-9 of a weight on average, as much
+// as the output's own rounding; a second half would cost half as many matrix operations again).
+// z and the sum of the rounded weights put the codes' 16 and lo in: o = sum w' (16 + code) +
+// sum p (lo + 8 step) - 24 sum w', so that the rounding counts for code - 8 only.
 template <int D>
-__global__ __launch_bounds__(256) void kv_prefill_kernel(KvArgs b, const bf16_t* q, int64_t q_stride, KvOut w, float c,
-                                                         KvCut cut) {
-    constexpr int RB = kKvPrefillRows, kStage = KvStage<D>::kBytes;
-    __shared__ __attribute__((aligned(1024))) uint8_t stage0[4 * kStage];
-    __shared__ __attribute__((aligned(1024))) uint8_t stage1[4 * kStage];
+struct KvRows {
+    static constexpr int S = D / 16, NB = D / 32, NQ = D == 256 ? 2 : 1;
+    static constexpr int kSlab = 8 * D, kCodes = 8 * kSlab, kStage = kCodes + 4 * 128 + 16;
+    static constexpr int kTable = 64 * 16;   // a wave's floats of a stage's tokens
+    u32x4 q[S];
+    f32x16_t o[NB];
+    float qsum, m, thr, l, z, s;
+    int limit, limit_all;
+    CodeConst cc;
+
+    __device__ __forceinline__ void load_q(const KvArgs& b, const KvSeq& sq, int h, const bf16_t* qp, int64_t stride,
+                                           int row0) {
+        const int hg = (threadIdx.x & 63) >> 5, r = row0 + (threadIdx.x & 31), rows = sq.rows * b.group;
+        qsum = 0.f;
+        if (r < rows) {
+            const bf16_t* p = qp + (int64_t)(sq.r0 + r / b.group) * stride + (int64_t)(h * b.group + r % b.group) * D +
+                              hg * (D / 2);
+#pragma unroll
+            for (int i = 0; i < S; ++i) q[i] = ld16(p + 8 * i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < S; ++i) q[i] = u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) qsum += bf16_lo(q[i][j]) + bf16_hi(q[i][j]);
+        qsum = sum_hg(qsum);
+        const int first = sq.len - sq.rows + 1;
+        limit = r < rows ? first + r / b.group : 0;
+        limit_all = row0 < rows ? first + row0 / b.group : 0;
+        m = 0.f;
+        thr = -INFINITY;   // (no token yet)
+        l = z = s = 0.f;
+#pragma unroll
+        for (int e = 0; e < NB; ++e)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[e][i] = 0.f;
+    }
+
+    // Keys and values of one block to its place in a stage: keys as [i][hg][token], values as
+    // [n][i] 16-byte units, the order in which the lanes read them.
+    static __device__ __forceinline__ void load(const uint8_t* k, const uint8_t* v, uint8_t* stage, int block) {
+        const int lane = threadIdx.x & 63;
+        uint8_t* to = stage + block * 2 * kSlab;
+        auto key = [](int u) { return (u & 15) * (D / 2) + ((u >> 4) & 1) * (D / 4) + (u >> 5) * 16; };
+        auto val = [](int u) { return (u & 15) * (D / 2) + (u >> 4) * 16; };
+        if constexpr (D == 64) {
+            global_load_lds16(lane < 32 ? k + key(lane) : v + val(lane & 31), to);
+        } else {
+#pragma unroll
+            for (int i = 0; i < D / 128; ++i) global_load_lds16(k + key(64 * i + lane), to + 1024 * i);
+#pragma unroll
+            for (int i = 0; i < D / 128; ++i) global_load_lds16(v + val(64 * i + lane), to + kSlab + 1024 * i);
+        }
+        if (lane < 32) global_load_lds4((lane < 16 ? k : v) + 8 * D + (lane & 15) * 4, stage + kCodes + block * 128);
+    }
+
+    // the floats of a stage's 64 tokens: key step and lo times c, value step, value lo + 8 step
+    static __device__ __forceinline__ void table(const uint8_t* stage, f32x4* tab, float c) {
+        const int lane = threadIdx.x & 63;
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(stage + kCodes) + (lane >> 4) * 32 + (lane & 15);
+        const uint32_t kw = w[0], vw = w[16];
+        const float st = bf16_lo(vw);
+        tab[lane] = f32x4{bf16_lo(kw) * c, bf16_hi(kw) * c, st, fmaf(8.f, st, bf16_hi(vw))};
+    }
+
+    // 32 tokens: blocks 2 u and 2 u + 1 of a stage, the first at position tok0; bit a of bad: block
+    // 2 u + a counts nothing
+    __device__ __forceinline__ void step(const uint8_t* stage, const f32x4* tab, int u, int tok0, int bad) {
+        const int lane = threadIdx.x & 63, lr = lane & 31, hg = lane >> 5;
+        f32x16_t x;
+        const float init = -16.f * qsum;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = init;
+        const uint8_t* kp = stage + (2 * u + (lr >> 4)) * 2 * kSlab + (hg * 16 + (lr & 15)) * 16;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            const u32x4 w = ld16(kp + i * 512);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const uint32_t word = w[y];
+                u32x4 kf;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) kf[j] = code_pair(cc, word, j);
+                x = mma32(kf, q[4 * i + y], x);
+            }
+        }
+        float st[16], zl[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const f32x4 f = tab[32 * u + 8 * (i / 4) + 4 * hg + i % 4];
+            x[i] = fmaf(x[i], f[0], fmaf(f[1], qsum, -m));
+            st[i] = f[2];
+            zl[i] = f[3];
+        }
+        if (__builtin_expect(tok0 + 32 > limit_all || bad, 0)) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int tok = tok0 + 8 * (i / 4) + 4 * hg + i % 4;
+                if (tok >= limit || ((bad >> (i / 8)) & 1)) {
+                    x[i] = -INFINITY;
+                    st[i] = zl[i] = 0.f;
+                }
+            }
+        }
+        float top = x[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
+        if (__ballot(top > thr)) {
+            float d = max_hg(top);
+            if (!(d > thr)) d = 0.f;   // (not this row, or it has no token yet)
+            else thr = 8.f;
+            const float al = __builtin_amdgcn_exp2f(-d);
+            m += d;
+            l *= al;
+            z *= al;
+            s *= al;
+#pragma unroll
+            for (int e = 0; e < NB; ++e)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[e][i] *= al;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] -= d;
+        }
+        u32x4 p[2];
+        const bf16x2_t one = __builtin_bit_cast(bf16x2_t, 0x3F803F80u);
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const float p0 = __builtin_amdgcn_exp2f(x[i]), p1 = __builtin_amdgcn_exp2f(x[i + 1]);
+            l += p0;
+            l += p1;
+            z = fmaf(p0, zl[i], z);
+            z = fmaf(p1, zl[i + 1], z);
+            const uint32_t w = pack2(p0 * st[i], p1 * st[i + 1]);
+            s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, w), one, s, false);
+            p[i / 8][i % 8 / 2] = w;
+        }
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            // the lane's words of block 2 u + a: token pairs 2 hg, 2 hg + 1, 4 + 2 hg, 5 + 2 hg of value
+            // column lane % 16, the half of its values that lane / 16 says
+            const uint8_t* vp = stage + (2 * (2 * u + a) + 1) * kSlab + (lane & 15) * 16;
+            const int sel = (lane >> 4) & 1;
+            uint32_t w[NQ][4];
+            if constexpr (D == 64) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const u32x2 v = *reinterpret_cast<const u32x2*>(vp + n * 256 + hg * 8);
+                    w[0][2 * n] = v[0] >> (8 * sel);
+                    w[0][2 * n + 1] = v[1] >> (8 * sel);
+                }
+            } else if constexpr (D == 128) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const uint32_t* v = reinterpret_cast<const uint32_t*>(vp + (2 * n + hg) * 256) + sel;
+                    w[0][2 * n] = v[0];
+                    w[0][2 * n + 1] = v[2];
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const uint32_t* v = reinterpret_cast<const uint32_t*>(vp + (4 * (n / 2) + 2 * hg + n % 2) * 256) + sel;
+                    w[0][n] = v[0];
+                    w[1][n] = v[2];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < NB; ++e) {
+                u32x4 vf;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) vf[n] = code_pair(cc, w[e / 4][n], e % 4);
+                o[e] = mma32(vf, p[a], o[e]);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void finish() {
+        l = sum_hg(l);
+        z = sum_hg(z) - 24.f * sum_hg(s);
+        if (thr < 0.f) m = -INFINITY;
+    }
+
+    // the row's values, four at a time: f(first value, values)
+    template <class F>
+    __device__ __forceinline__ void each4(F f) const {
+        const int hg = (threadIdx.x & 63) >> 5;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int col = 8 * (i / 4) + 4 * hg + i % 4;
+            if constexpr (D == 64) {
+                f(col * 4, f32x4{o[0][i] + z, o[1][i] + z, o[0][i + 8] + z, o[1][i + 8] + z});
+            } else {
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        f(col * (D / 16) + 8 * n + 4 * h, f32x4{o[4 * n][i + 8 * h] + z, o[4 * n + 1][i + 8 * h] + z,
+                                                                o[4 * n + 2][i + 8 * h] + z, o[4 * n + 3][i + 8 * h] + z});
+            }
+        }
+    }
+};
+
+template <int D>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_prefill_kernel(KvArgs b, const bf16_t* q, int64_t q_stride,
+                                                                           KvOut w, float c, KvCut cut) {
+    using Rows = KvRows<D>;
+    constexpr int RB = kKvPrefillRows;
+    __shared__ __attribute__((aligned(1024))) uint8_t stage0[Rows::kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t stage1[Rows::kStage];
+    __shared__ f32x4 tabs[4][64];
     __shared__ KvLine line;
     kv_line(b, cut, line);
-    const int li = threadIdx.x & 15;
+    const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int worker = blockIdx.x;
     const KvPieces pieces(uniform64(line.before[256]), cut.workers);
@@ -937,25 +1171,81 @@ __global__ __launch_bounds__(256) void kv_prefill_kernel(KvArgs b, const bf16_t*
     if (pos < end) at.seek(b, cut, line, pos);
     while (pos < end) {
         const int h = at.pair % b.kv_heads, tile0 = at.pair / b.kv_heads * RB, rows = at.q.rows * b.group;
-        const int row0 = tile0 + 16 * wave, stop = (int)min((int64_t)at.steps, at.off + (end - pos));
+        const int row0 = tile0 + 32 * wave, stop = (int)min((int64_t)at.steps, at.off + (end - pos));
         if (at.off == 0 && stop < at.steps) {
             const int last = pieces.holder(pos + at.steps - 1), none = (last + 4) >> 2;
             entry = KvMerge{last, tile0, min(RB, rows - tile0), at.q.r0, h, none, none, 0};
         }
-        if (row0 < rows) {
-            const int seen = max(0, at.q.len - at.q.rows + 1 + (min(rows, row0 + 16) - 1) / b.group);
-            KvWave<D, 1, false> wv;
-            wv.load_q(b, at.s, at.q, h, q, q_stride, row0);
-            wv.run(b, stage0 + wave * kStage, stage1 + wave * kStage, at.off, min(kv_steps(seen), stop), c);
-            wv.finish();
-            const int slot = 2 * worker + (at.off == 0), rt = 16 * wave + li;
-            if (row0 + li >= rows) {
-            } else if (at.off == 0 && stop == at.steps) {
-                wv.store(out_row<D>(b, w, at.q.r0, h, row0 + li));
-            } else {
-                wv.put_part(part_row<D>(w, RB, slot, rt), part_ml<D>(w, RB, slot, rt));
+        // tokens that the tile's last row sees, and the wave's
+        auto sees = [&](int row) { return max(0, at.q.len - at.q.rows + 1 + row / b.group); };
+        const int end_tok = min(32 * stop, sees(min(rows, tile0 + RB) - 1));
+        const int wave_end = row0 < rows ? min(end_tok, sees(min(rows, row0 + 32) - 1)) : 0;
+        const int first = 32 * at.off, n = (max(0, end_tok - first) + 63) / 64;
+        const int ks = 2 * h, vs = 2 * h + 1;
+        const int64_t koff = (int64_t)(ks % b.slabs_per_page) * kv_slab_bytes(D);
+        const int64_t voff = (int64_t)(vs % b.slabs_per_page) * kv_slab_bytes(D);
+        Rows r;
+        r.load_q(b, at.q, h, q, q_stride, row0);
+        int pk = -1, pv = -1;   // lane j: the pages of this wave's block of stage j of 64
+        auto pages = [&](int j0) {
+            const int blk = first / kKvBlock + 4 * (j0 + lane) + wave;
+            pk = pv = -1;
+            if (kKvBlock * blk < end_tok) {
+                pk = *kv_entry(b, at.s, blk, ks);
+                pv = *kv_entry(b, at.s, blk, vs);
+            }
+        };
+        auto issue = [&](int j, uint8_t* stage) {
+            if ((j & 63) == 0) pages(j);
+            const int k = __builtin_amdgcn_readlane(pk, j & 63), v = __builtin_amdgcn_readlane(pv, j & 63);
+            const bool ok = kv_page_ok(b, k) && kv_page_ok(b, v);
+            Rows::load(b.pages + (ok ? k : 0) * b.page_bytes + koff, b.pages + (ok ? v : 0) * b.page_bytes + voff, stage,
+                       wave);
+            if (lane == 0) reinterpret_cast<int*>(stage + Rows::kCodes + 512)[wave] = !ok;
+        };
+        if (n > 0) issue(0, stage0);
+#pragma unroll 1
+        for (int j = 0; j < n; j += 2) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (j + x >= n) break;
+                uint8_t* now = x ? stage1 : stage0;
+                wait_vmcnt<0>();
+                wait_lgkm0();
+                __builtin_amdgcn_s_barrier();   // the stage is there, and every wave has done with the other
+                landed();
+                if (j + x + 1 < n) issue(j + x + 1, x ? stage0 : stage1);
+                const int tok = first + 64 * (j + x);
+                if (tok < wave_end) {
+                    Rows::table(now, tabs[wave], c);
+                    const u32x4 f = ld16(now + Rows::kCodes + 512);
+                    const int bad = __builtin_amdgcn_readfirstlane(f[0] | f[1] << 1 | f[2] << 2 | f[3] << 3);
+                    r.step(now, tabs[wave], 0, tok, bad & 3);
+                    if (tok + 32 < wave_end) r.step(now, tabs[wave], 1, tok + 32, bad >> 2);
+                }
             }
         }
+        r.finish();
+        const int rt = 32 * wave + (lane & 31);
+        if (tile0 + rt < rows) {
+            if (at.off == 0 && stop == at.steps) {
+                bf16_t* o = out_row<D>(b, w, at.q.r0, h, tile0 + rt);
+                const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
+                r.each4([&](int d, const f32x4& v) {
+                    *reinterpret_cast<u32x2*>(o + d) = u32x2{pack2(v[0] * inv, v[1] * inv), pack2(v[2] * inv, v[3] * inv)};
+                });
+            } else {
+                const int slot = 2 * worker + (at.off == 0);
+                float* p = part_row<D>(w, RB, slot, rt);
+                r.each4([&](int d, const f32x4& v) { *reinterpret_cast<f32x4*>(p + d) = v; });
+                if (lane < 32) {
+                    float* ml = part_ml<D>(w, RB, slot, rt);
+                    ml[0] = r.m / c;   // (parts are joined at the scale of the scores)
+                    ml[1] = r.l;
+                }
+            }
+        }
+        __syncthreads();   // (the stages are free)
         pos += stop - at.off;
         if (pos < end) at.next(b, cut);
     }
@@ -1103,7 +1393,7 @@ hipError_t attention(const KvArgs& b, const bf16_t* q, int64_t q_stride, bf16_t*
         hipLaunchKernelGGL(kv_merge_kernel<D>, dim3(grid), dim3(256), 0, s, b, w, c, 1 << rb_shift, most_rows);
         return hipGetLastError();
     };
-    static_assert(kKvRowTile == 16 && kKvPrefillRows == 64, "row tiles");
+    static_assert(kKvRowTile == 16 && kKvPrefillRows == 128, "row tiles");
     // few rows: as many columns of a matrix operation a row as there are
     const int n = kv_workers(D);
     if (most <= 1) return go(0, kKvAll, n, 4, kv_decode_kernel<D, 8, true>);
@@ -1112,7 +1402,7 @@ hipError_t attention(const KvArgs& b, const bf16_t* q, int64_t q_stride, bf16_t*
     if (most <= 8) return go(3, kKvAll, n, 4, kv_decode_kernel<D, 2, false>);
     if (most <= 16) return go(4, kKvAll, n, 4, kv_decode_kernel<D, 1, false>);
     hipError_t e = go(4, kKvFew, n, 4, kv_decode_kernel<D, 1, false>);
-    return e != hipSuccess ? e : go(6, kKvMany, n / 4, 1, kv_prefill_kernel<D>);
+    return e != hipSuccess ? e : go(7, kKvMany, kKvPrefillWorkers, 1, kv_prefill_kernel<D>);
 }
 
 }  // namespace
