@@ -56,27 +56,30 @@ class KvBatch:
         if len({row_start.device, ctx_len.device, page_table.device}) != 1:
             raise ValueError("row_start, ctx_len and page_table must be on one device")
         self.row_start, self.ctx_len, self.page_table = row_start, ctx_len, page_table
+        self.device, self.index = row_start.device, row_start.get_device()
         self.pages_per_block = page_table.shape[2]
         self.n_rows = n_rows
+        self.dtype = torch.bfloat16
         self.c = L.lora_kv_batch(n_heads, n_kv_heads, head_dim, n_seqs, n_rows, n_rows if max_rows is None else max_rows,
                                  page_table.shape[1], 0, row_start.data_ptr(), ctx_len.data_ptr(),
                                  page_table.data_ptr())
+        self.heads = (n_heads, head_dim), (n_kv_heads, head_dim)
 
-    def rows(self, name: str, t, heads: int) -> int:
-        """The row stride of t, checked to be this batch's rows of so many heads."""
-        import torch
-        c = self.c
-        if t.device != self.row_start.device or t.dtype != torch.bfloat16:
-            raise ValueError(f"{name} must be bfloat16 on {self.row_start.device}")
-        if t.dim() == 2 and t.shape[1] == heads * c.head_dim:
-            inner = t.stride(1) == 1
-        elif t.dim() == 3 and t.shape[1:] == (heads, c.head_dim):
-            inner = t.stride(2) == 1 and (heads == 1 or t.stride(1) == c.head_dim)
+    def rows(self, name: str, t, kv: bool) -> int:
+        """The row stride of t, checked to be this batch's rows of the query (or KV) heads."""
+        heads, dim = self.heads[kv]
+        if t.get_device() != self.index or t.dtype is not self.dtype:
+            raise ValueError(f"{name} must be {self.dtype} on {self.device}")
+        shape, st = t.shape, t.stride()
+        if len(shape) == 3 and shape[1] == heads and shape[2] == dim:
+            inner = st[2] == 1 and (heads == 1 or st[1] == dim)
+        elif len(shape) == 2 and shape[1] == heads * dim:
+            inner = st[1] == 1
         else:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, not [rows, {heads}, {c.head_dim}] or [rows, {heads * c.head_dim}]")
-        if t.shape[0] != self.n_rows or not inner:
+            raise ValueError(f"{name}: shape {tuple(shape)}, not [rows, {heads}, {dim}] or [rows, {heads * dim}]")
+        if shape[0] != self.n_rows or not inner:
             raise ValueError(f"{name}: {self.n_rows} rows of contiguous heads are needed")
-        return t.stride(0) if self.n_rows > 1 else heads * c.head_dim
+        return st[0] if self.n_rows > 1 else heads * dim
 
 
 class DevicePool:
@@ -112,6 +115,7 @@ class DevicePool:
                 desc.stage_bytes = stage_bytes
         self.pool = L.lora_pool_create(desc, keep)
         self._host: Dict[int, tuple] = {}
+        self._kv_pages: Dict[tuple, int] = {}
 
     # -- adapters ---------------------------------------------------------------
     def page_in(self, adapter_id: int, rank: int, alpha: float, A_blob: Optional[np.ndarray] = None,
@@ -196,57 +200,68 @@ class DevicePool:
     # -- keys and values in the pages ----------------------------------------------
     def kv_pages_per_block(self, n_kv_heads: int, head_dim: int) -> int:
         """Pages of 16 tokens' keys and values in one layer."""
-        return L.lora_kv_pages_per_block(self.pool, n_kv_heads, head_dim)
+        n = self._kv_pages.get((n_kv_heads, head_dim))
+        if n is None:
+            n = self._kv_pages[n_kv_heads, head_dim] = L.lora_kv_pages_per_block(self.pool, n_kv_heads, head_dim)
+        return n
 
     def kv_workspace(self, batch: KvBatch):
         """A workspace for kv_attention; calls that may overlap need one each."""
         import torch
-        return torch.empty(L.lora_kv_workspace_bytes(batch.c), dtype=torch.uint8, device=batch.row_start.device)
+        return torch.empty(L.lora_kv_workspace_bytes(batch.c), dtype=torch.uint8, device=batch.device)
 
-    def _kv_check(self, batch: KvBatch, stream):
+    def _kv_call(self, batch: KvBatch, stream, call) -> None:
+        """call(stream) on the batch's GPU, whichever is current."""
         import torch
-        dev = batch.row_start.device
-        if self.pages is None or dev != self.pages.device:
-            raise ValueError(f"the batch is on {dev}, the pool on {self.pages.device if self.pages is not None else None}")
-        need = self.kv_pages_per_block(batch.c.n_kv_heads, batch.c.head_dim)
+        if self.pages is None or batch.index != self.pages.get_device():
+            raise ValueError(f"the batch is on {batch.device}, the pool on {None if self.pages is None else self.pages.device}")
+        need = self.kv_pages_per_block(batch.heads[1][0], batch.heads[1][1])
         if batch.pages_per_block != need:
             raise ValueError(f"page_table has {batch.pages_per_block} pages a block, {need} are needed")
-        return torch.cuda.current_stream(dev) if stream is None else stream
+        if stream is None:
+            stream = L.current_stream(batch.index)
+        if torch.cuda.current_device() == batch.index:
+            call(stream)
+        else:
+            with torch.cuda.device(batch.index):
+                call(stream)
 
     def kv_append(self, batch: KvBatch, k, v, q=None, q_out=None, k_out=None, v_out=None, cos_sin=None,
                   interleaved: bool = False, stream=None) -> None:
         """Append the rows' keys and values to their pages; q, k turned by cos_sin [positions, rot_dim]."""
         import torch
-        st = self._kv_check(batch, stream)
-        c, r = batch.c, L.lora_kv_rows()
-        for name, t, heads in (("k", k, c.n_kv_heads), ("v", v, c.n_kv_heads), ("q", q, c.n_heads),
-                               ("q_out", q_out, c.n_heads), ("k_out", k_out, c.n_kv_heads),
-                               ("v_out", v_out, c.n_kv_heads)):
-            if t is not None:
-                setattr(r, name, t.data_ptr())
-                setattr(r, name + "_stride", batch.rows(name, t, heads))
+        rows = batch.rows
+        r = L.lora_kv_rows(k.data_ptr(), v.data_ptr())
+        r.k_stride, r.v_stride = rows("k", k, True), rows("v", v, True)
+        if q is not None:
+            r.q, r.q_stride = q.data_ptr(), rows("q", q, False)
+        if q_out is not None:
+            r.q_out, r.q_out_stride = q_out.data_ptr(), rows("q_out", q_out, False)
+        if k_out is not None:
+            r.k_out, r.k_out_stride = k_out.data_ptr(), rows("k_out", k_out, True)
+        if v_out is not None:
+            r.v_out, r.v_out_stride = v_out.data_ptr(), rows("v_out", v_out, True)
         pos = rot = 0
         if cos_sin is not None:
-            if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or \
-                    cos_sin.device != batch.row_start.device:
+            if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or \
+                    cos_sin.get_device() != batch.index:
                 raise ValueError("cos_sin must be a contiguous float32 [positions, rot_dim] tensor on the batch's device")
             pos, rot = cos_sin.shape
-        with torch.cuda.device(batch.row_start.device):
-            L.lora_kv_append(self.pool, c, r, cos_sin, rot, pos, interleaved, st)
+        self._kv_call(batch, stream,
+                      lambda st: L.lora_kv_append(self.pool, batch.c, r, cos_sin, rot, pos, interleaved, st))
 
     def kv_attention(self, batch: KvBatch, q, out, scale: Optional[float] = None, workspace=None, stream=None) -> None:
         """Attention of the batch's rows (q already turned) over the pages; scale None: head_dim ** -0.5."""
-        import torch
-        st = self._kv_check(batch, stream)
-        c = batch.c
         if workspace is None:
             raise ValueError("kv_attention needs a workspace (kv_workspace)")
-        if workspace.device != batch.row_start.device or not workspace.is_contiguous():
+        if workspace.get_device() != batch.index or not workspace.is_contiguous():
             raise ValueError("the workspace must be contiguous and on the batch's device")
-        with torch.cuda.device(batch.row_start.device):
-            L.lora_kv_attention(self.pool, c, q, batch.rows("q", q, c.n_heads), out, batch.rows("out", out, c.n_heads),
-                                c.head_dim ** -0.5 if scale is None else scale, workspace,
-                                workspace.numel() * workspace.element_size(), st)
+        qs, os_ = batch.rows("q", q, False), batch.rows("out", out, False)
+        if scale is None:
+            scale = batch.heads[0][1] ** -0.5
+        size = workspace.numel() * workspace.element_size()
+        self._kv_call(batch, stream,
+                      lambda st: L.lora_kv_attention(self.pool, batch.c, q, qs, out, os_, scale, workspace, size, st))
 
     def linear_decode(self, layer: int, proj: int, x, w0, y, token_slot, stream=None) -> None:
         L.lora_linear_decode(self.pool, layer, proj, x, w0, y, token_slot, stream)
