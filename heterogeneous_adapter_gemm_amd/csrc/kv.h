@@ -33,6 +33,7 @@ struct KvAppendArgs {
     int32_t rot, interleaved;
 };
 
+constexpr int kKvAppendBlocks = 1280;    // append workgroups that run at once
 constexpr int kKvRowTile = 16;           // query rows of a decode segment
 constexpr int kKvPrefillRows = 128;      // query rows of a prefill segment
 // Waves that share the attention's work, as many as run at once by their registers: on each of

@@ -86,7 +86,7 @@ __device__ __forceinline__ void put(bf16_t* y, float* ybase, const int32_t* row_
 // ---------------------------------------------------------------- up to 16 rows
 
 // One workgroup per 16 columns of y: its eight waves take the 128-deep pieces of K in turn (the
-// codes of the next three in flight, x of the next one), and their sums meet in LDS in wave
+// codes and x of the next three in flight), and their sums meet in LDS in wave
 // order.  Bound by reading the codes once; at a few microseconds, by the latency of that.
 constexpr int kRowWaves = 8;
 
@@ -128,19 +128,24 @@ __global__ __launch_bounds__(64 * kRowWaves) void gemm_w4_rows_kernel(
     f32x4 acc{0.f, 0.f, 0.f, 0.f};
     constexpr int PF = 4, kStep = 128 * kRowWaves;
     Codes p[PF];
-    Rows r[2];
+    Rows r[PF];
     const int k0 = wave * 128, last = K - 128;
 #pragma unroll
-    for (int i = 0; i < PF; ++i) load(min(k0 + i * kStep, last), p[i]);
-    load_x(min(k0, last), r[0]);
+    for (int i = 0; i < PF; ++i) {
+        load(min(k0 + i * kStep, last), p[i]);
+        load_x(min(k0 + i * kStep, last), r[i]);
+    }
     for (int kb0 = k0; kb0 < K; kb0 += PF * kStep) {
 #pragma unroll
         for (int i = 0; i < PF; ++i) {
             const int kb = kb0 + i * kStep;
             if (kb >= K) break;
             const Codes now = p[i];
-            load_x(min(kb + kStep, last), r[(i + 1) & 1]);
-            load(min(kb + PF * kStep, last), p[i]);
+            const Rows xr = r[i];
+            if (kb + PF * kStep < K) {
+                load(kb + PF * kStep, p[i]);
+                load_x(kb + PF * kStep, r[i]);
+            }
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 const float sc = half_lo(now.s[g]), corr = -sc * (16.f + half_hi(now.s[g]));
@@ -148,7 +153,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void gemm_w4_rows_kernel(
                 float xs = 0.f;
 #pragma unroll
                 for (int t = 0; t < W; ++t) {
-                    const u32x4 v = r[i & 1].x[g][t];
+                    const u32x4 v = xr.x[g][t];
                     d = mma_step(code_order(v), code_values(cc, now.c[g][t]), d, bf16_t{});
                     xs = add_x(v, xs);
                 }
@@ -304,7 +309,7 @@ __device__ __forceinline__ int row32(int i) { return 8 * (i / 4) + 4 * ((threadI
 // pieces of K in turn, each with its own place for x in LDS (two pieces, the next one in flight)
 // and no barrier until their sums meet there.
 template <int G, int MB, int NB>
-__global__ __launch_bounds__(256) void gemm_w4_decode_kernel(const bf16_t* __restrict__ x, const uint8_t* __restrict__ q,
+__global__ __launch_bounds__(256, 2) void gemm_w4_decode_kernel(const bf16_t* __restrict__ x, const uint8_t* __restrict__ q,
                                                              const uint32_t* __restrict__ sz, bf16_t* __restrict__ y, int M,
                                                              int N, int K, const int32_t* __restrict__ row_slot,
                                                              float* __restrict__ ybase) {
@@ -329,8 +334,10 @@ __global__ __launch_bounds__(256) void gemm_w4_decode_kernel(const bf16_t* __res
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
     const int n = (K / 128 - wave + 3) / 4;   // pieces of this wave
+    // (each workgroup begins at a piece of its own, so that they do not all read one slice of x at once)
+    const int shift = n > 0 ? (int)(blockIdx.x % n) : 0;
     auto issue = [&](int j, uint8_t* to) {
-        const int kb = (wave + 4 * j) * 128;
+        const int kb = (wave + 4 * (j + shift < n ? j + shift : j + shift - n)) * 128;
         load_rows(x, m0, M, K, kb, to, 0, kRows / 4);
         cols.load(kb, stc);
     };
