@@ -99,6 +99,14 @@ __device__ __forceinline__ void landed() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// v, four issue slots after what wrote it: another kind of instruction may read a dot product's
+// result three slots later at the earliest, and the compiler does not keep that distance to a matrix
+// operation.
+__device__ __forceinline__ float settled(float v) {
+    asm volatile("s_nop 3" : "+v"(v));
+    return v;
+}
+
 // s_waitcnt lgkmcnt(0), the other counters unconstrained, and nothing moved over it
 __device__ __forceinline__ void wait_lgkm0() {
     landed();

@@ -57,6 +57,17 @@ __device__ __forceinline__ f32x16 mma32(const u32x4& a, const u32x4& b, f32x16 c
 __device__ __forceinline__ float half_lo(uint32_t w) { return (float)__builtin_bit_cast(_Float16, (uint16_t)w); }
 __device__ __forceinline__ float half_hi(uint32_t w) { return (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16)); }
 
+// A group's scale, and what its zero point and the codes' 16 take away per unit of x.  (The scale in
+// a register of its own: as a half inside a multiply-add it costs the longer instruction.)
+struct Scale {
+    float scale, corr;
+    __device__ __forceinline__ explicit Scale(uint32_t w) {
+        scale = half_lo(w);
+        asm volatile("" : "+v"(scale));
+        corr = -scale * (16.f + half_hi(w));
+    }
+};
+
 template <int W>
 __device__ __forceinline__ void ld_words(const uint8_t* p, uint32_t (&o)[W]) {
     if constexpr (W == 1) {
@@ -157,7 +168,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void gemm_w4_rows_kernel(
                     d = mma_step(code_order(v), code_values(cc, now.c[g][t]), d, bf16_t{});
                     xs = add_x(v, xs);
                 }
-                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(xs, corr, acc, 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(settled(xs), corr, acc, 0, 0, 0);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[j] = fmaf(sc, d[j], acc[j]);
             }
@@ -290,13 +301,15 @@ __device__ __forceinline__ void mul_piece(const uint8_t* xs, int r0, const typen
             }
         }
 #pragma unroll
+        for (int a = 0; a < MB; ++a) sum[a] = settled(sum[a]);
+#pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const float sc = half_lo(p.s[b][g]), corr = -sc * (16.f + half_hi(p.s[b][g]));
+            const Scale sc(p.s[b][g]);
 #pragma unroll
             for (int a = 0; a < MB; ++a) {
-                acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(sum[a], corr, acc[a][b], 0, 0, 0);
+                acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(sum[a], sc.corr, acc[a][b], 0, 0, 0);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[a][b][i] = fmaf(sc, d[a][b][i], acc[a][b][i]);
+                for (int i = 0; i < 16; ++i) acc[a][b][i] = fmaf(sc.scale, d[a][b][i], acc[a][b][i]);
             }
         }
     }
@@ -305,79 +318,144 @@ __device__ __forceinline__ void mul_piece(const uint8_t* xs, int r0, const typen
 // Row of register i of a 32 x 32 block
 __device__ __forceinline__ int row32(int i) { return 8 * (i / 4) + 4 * ((threadIdx.x & 63) >> 5) + i % 4; }
 
-// Decode batches: 32 MB rows by 32 NB columns a workgroup, its four waves taking the 128-deep
-// pieces of K in turn, each with its own place for x in LDS (two pieces, the next one in flight)
-// and no barrier until their sums meet there.
+// Decode batches: 32 MB rows by 32 NB columns a workgroup, its eight waves taking the 128-deep
+// pieces of K in turn, in halves, each with its own place for x in LDS (two halves, the next one in
+// flight) and no barrier until their sums meet there.  Two waves a SIMD, so that one's conversions run
+// beside the other's matrix operations.
+constexpr int kDecodeWaves = 8;
+
 template <int G, int MB, int NB>
-__global__ __launch_bounds__(256, 2) void gemm_w4_decode_kernel(const bf16_t* __restrict__ x, const uint8_t* __restrict__ q,
-                                                             const uint32_t* __restrict__ sz, bf16_t* __restrict__ y, int M,
-                                                             int N, int K, const int32_t* __restrict__ row_slot,
-                                                             float* __restrict__ ybase) {
-    using Cols = W4Cols<G, NB>;
-    constexpr int kRows = 32 * MB, kStage = kRows * 256;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds0[4 * kStage];
-    __shared__ __attribute__((aligned(1024))) uint8_t lds1[4 * kStage];
-    __shared__ __attribute__((aligned(1024))) uint8_t ldsc[4 * Cols::kBytes];
-    const int lane = threadIdx.x & 63;
+__global__ __launch_bounds__(64 * kDecodeWaves, 2) void gemm_w4_decode_kernel(
+    const bf16_t* __restrict__ x, const uint8_t* __restrict__ q, const uint32_t* __restrict__ sz, bf16_t* __restrict__ y,
+    int M, int N, int K, const int32_t* __restrict__ row_slot, float* __restrict__ ybase) {
+    constexpr int kRows = 32 * MB, kStage = kRows * 128, W = kDecodeWaves;
+    constexpr int GH = G < 64 ? G : 64, NG = 64 / GH, S = GH / 16;   // group's part of a half, parts of a half, steps of a part
+    constexpr int kSums = MB * NB * 16 * 256;                       // a wave's sums
+    constexpr int kLds = 2 * kStage > kSums ? 2 * kStage : kSums;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[W * kLds];
+    const int lane = threadIdx.x & 63, lr = lane & 31, hg = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = blockIdx.x * 32 * NB, m0 = blockIdx.y * kRows;
-    const Cols cols(q, sz, n0, N, K);
     const CodeConst cc;
-    uint8_t* st0 = lds0 + wave * kStage;
-    uint8_t* st1 = lds1 + wave * kStage;
-    uint8_t* stc = ldsc + wave * Cols::kBytes;
-    f32x16 acc[MB][NB];
+    uint8_t* place = lds + wave * 2 * kStage;
+    const uint8_t* qn[NB];
+    const uint32_t* sn[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int64_t c = min(n0 + 32 * b + lr, N - 1);
+        qn[b] = q + c * (K / 2) + hg * (GH / 4);
+        sn[b] = sz + c * (K / G);
+    }
+    // x: a wave-load fills eight rows of 64 values; 16-byte chunk i of row r in slot i ^ (r / 2 % 8)
+    const bf16_t* xl[4 * MB];
+#pragma unroll
+    for (int i = 0; i < 4 * MB; ++i) {
+        const int r = 8 * i + (lane >> 3);
+        xl[i] = x + (int64_t)min(m0 + r, M - 1) * K + ((lane & 7) ^ ((r >> 1) & 7)) * 8;
+    }
+    struct Codes {
+        uint32_t c[NB][NG][S], s[NB][NG];
+    };
+    auto issue = [&](int kb, int half, Codes& p) {
+#pragma unroll
+        for (int i = 0; i < 4 * MB; ++i) global_load_lds16(xl[i] + kb, place + half * kStage + i * 1024);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                ld_words(qn[b] + (kb + g * GH) / 2, p.c[b][g]);
+                p.s[b][g] = sn[b][(kb + g * GH) / G];
+            }
+    };
+    f32x16 acc[MB][NB], d[MB][NB];
+    float sum[MB];
 #pragma unroll
     for (int a = 0; a < MB; ++a)
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
-    const int n = (K / 128 - wave + 3) / 4;   // pieces of this wave
+    auto work = [&](int half, const Codes& p) {
+        const uint8_t* xs = place + half * kStage;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            if (G <= 64 || half == 0) {
+#pragma unroll
+                for (int a = 0; a < MB; ++a) {
+                    sum[a] = 0.f;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) d[a][b][i] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < S; ++t) {
+                u32x4 cf[NB];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) cf[b] = code_values(cc, p.c[b][g][t]);
+#pragma unroll
+                for (int a = 0; a < MB; ++a) {
+                    const u32x4 v = ld16(xs + (32 * a + lr) * 128 + ((g * (GH / 8) + hg * S + t) ^ ((lr >> 1) & 7)) * 16);
+                    sum[a] = add_x(v, sum[a]);
+                    const u32x4 xf = code_order(v);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) d[a][b] = mma32(xf, cf[b], d[a][b]);
+                }
+            }
+            if (G <= 64 || half == 1) {
+#pragma unroll
+                for (int a = 0; a < MB; ++a) sum[a] = settled(sum[a]);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const Scale sc(p.s[b][g]);
+#pragma unroll
+                    for (int a = 0; a < MB; ++a) {
+                        acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(sum[a], sc.corr, acc[a][b], 0, 0, 0);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[a][b][i] = fmaf(sc.scale, d[a][b][i], acc[a][b][i]);
+                    }
+                }
+            }
+        }
+    };
+    const int n = (K / 128 - wave + W - 1) / W;   // pieces of this wave
     // (each workgroup begins at a piece of its own, so that they do not all read one slice of x at once)
     const int shift = n > 0 ? (int)(blockIdx.x % n) : 0;
-    auto issue = [&](int j, uint8_t* to) {
-        const int kb = (wave + 4 * (j + shift < n ? j + shift : j + shift - n)) * 128;
-        load_rows(x, m0, M, K, kb, to, 0, kRows / 4);
-        cols.load(kb, stc);
-    };
-    if (n > 0) issue(0, st0);
+    auto at = [&](int j) { return (wave + W * (j + shift < n ? j + shift : j + shift - n)) * 128; };
+    Codes p[2];
+    if (n > 0) issue(at(0), 0, p[0]);
 #pragma unroll 1
-    for (int j = 0; j < n; j += 2) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if (j + u >= n) break;
-            wait_vmcnt<0>();
-            landed();
-            typename Cols::Codes p;
-            cols.read(stc, p);
-            // the codes are in registers and the other place has been used up: the next piece goes there
-            wait_lgkm0();
-            if (j + u + 1 < n) issue(j + u + 1, u ? st0 : st1);
-            mul_piece<G, MB, NB>(u ? st1 : st0, 0, p, cc, acc);
-        }
+    for (int j = 0; j < n; ++j) {
+        const int kb = at(j);
+        wait_vmcnt<0>();
+        wait_lgkm0();   // (likewise the second's, a piece ago)
+        issue(kb + 64, 1, p[1]);
+        work(0, p[0]);
+        wait_vmcnt<0>();
+        wait_lgkm0();   // the first half's place has been read
+        if (j + 1 < n) issue(at(j + 1), 0, p[0]);
+        work(1, p[1]);
     }
-    // the waves' sums, 16 registers of a block at a time: [wave][i][lane]
-    float* part = reinterpret_cast<float*>(lds0);
-    static_assert(4 * kStage >= 4 * 16 * 64 * 4, "a block's sums fit");
+    // the waves' sums: [wave][block][i][lane]
+    __syncthreads();
+    float* part = reinterpret_cast<float*>(lds);
 #pragma unroll
     for (int a = 0; a < MB; ++a)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            __syncthreads();
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) part[(wave * 16 + i) * 64 + lane] = acc[a][b][i];
-            __syncthreads();
+            for (int i = 0; i < 16; ++i) part[wave * (kSums / 4) + ((a * NB + b) * 16 + i) * 64 + lane] = acc[a][b][i];
+    __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int reg = 4 * wave + i;
-                float v = 0.f;
+    for (int e = 0; e < MB * NB * 16 / W; ++e) {
+        const int reg = e * W + wave, i = reg & 15, a = reg / 16 / NB, b = reg / 16 % NB;
+        float v = 0.f;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) v += part[(w * 16 + reg) * 64 + lane];
-                const int m = m0 + 32 * a + row32(reg), c = n0 + 32 * b + (lane & 31);
-                if (m < M && c < N) put(y, ybase, row_slot, m, c, N, v);
-            }
-        }
+        for (int w = 0; w < W; ++w) v += part[w * (kSums / 4) + reg * 64 + lane];
+        const int m = m0 + 32 * a + row32(i), c = n0 + 32 * b + lr;
+        if (m < M && c < N) put(y, ybase, row_slot, m, c, N, v);
+    }
 }
 
 // Long batches: 128 x 128 of y a workgroup, 64 x 64 a wave; the 128-deep pieces of x go to LDS
@@ -392,9 +470,12 @@ __global__ __launch_bounds__(256, 2) void gemm_w4_long_kernel(const bf16_t* __re
     __shared__ __attribute__((aligned(1024))) uint8_t lds0[128 * 256];
     __shared__ __attribute__((aligned(1024))) uint8_t lds1[128 * 256];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int row_blocks = (M + 127) / 128;
+    const int row_blocks = (M + 127) / 128, col_blocks = (N + 127) / 128;
     const int lid = xcd_logical(blockIdx.x, gridDim.x);
-    const int m0 = (lid % row_blocks) * 128, n0 = (lid / row_blocks) * 128 + (wave & 1) * 64;
+    // strips of four row blocks, a column block after another (a block of x has four times the bytes
+    // of a block of codes: so the tiles that run at once share most of either)
+    const int strip = lid / (4 * col_blocks), in = lid - strip * 4 * col_blocks, high = min(4, row_blocks - 4 * strip);
+    const int m0 = (4 * strip + in % high) * 128, n0 = (in / high) * 128 + (wave & 1) * 64;
     const int r0 = (wave >> 1) * 64;
     const Cols cols(q, sz, n0, N, K);
     const CodeConst cc;
@@ -456,9 +537,9 @@ static hipError_t gemm_w4(const bf16_t* x, const uint8_t* q, const uint32_t* sz,
     if (M <= 16) return go(gemm_w4_rows_kernel<G>, cdiv(N, 16), 1, 64 * kRowWaves);
     const int64_t tiles = cdiv(M, 128) * cdiv(N, 128);
     if (M > 64 && tiles >= 128) return go(gemm_w4_long_kernel<G>, tiles, 1, 256);
-    if (M <= 32) return go(gemm_w4_decode_kernel<G, 1, 1>, cdiv(N, 32), 1, 256);
-    if (N >= 64 * 160) return go(gemm_w4_decode_kernel<G, 2, 2>, cdiv(N, 64), cdiv(M, 64), 256);
-    return go(gemm_w4_decode_kernel<G, 2, 1>, cdiv(N, 32), cdiv(M, 64), 256);
+    if (M <= 32) return go(gemm_w4_decode_kernel<G, 1, 1>, cdiv(N, 32), 1, 64 * kDecodeWaves);
+    if (N >= 64 * 160) return go(gemm_w4_decode_kernel<G, 2, 2>, cdiv(N, 64), cdiv(M, 64), 64 * kDecodeWaves);
+    return go(gemm_w4_decode_kernel<G, 2, 1>, cdiv(N, 32), cdiv(M, 64), 64 * kDecodeWaves);
 }
 
 hipError_t launch_gemm_w4(const void* x, const void* q, const void* sz, int32_t group, void* y, int64_t M, int64_t N,
