@@ -4,8 +4,8 @@
 // group of 32, 64 or 128 consecutive k, fp32 accumulation.
 //
 // The matrix cores run bf16 on the codes themselves: a nibble put in the top
-// four bits of bf16's mantissa stands for 16 + code exactly, so a code needs a
-// shift and one and-or, and no rounding.  Per group, fp32: y += scale * acc -
+// four bits of bf16's mantissa stands for 16 + code exactly, so two codes need a
+// multiplication and one and-or, and no rounding.  Per group, fp32: y += scale * acc -
 // scale * (16 + zero) * sum(x): the second term is one fp32 matrix operation of
 // each lane's own sum of its x.
 //
@@ -21,21 +21,18 @@ namespace {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// (16 + nibble k, 16 + nibble k + 4) of w as two bf16; the constants in registers (a
-// three-operand and-or takes none of its own)
+// The codes of w as bf16, 16 + code each, in their order: a byte times 2^3 + 2^15 has its low nibble in
+// bits 3 to 6 and its high one in bits 19 to 22 (one instruction, the byte chosen in it).  The constants
+// in registers: a three-operand and-or takes none of its own.
 struct CodeConst {
-    uint32_t mask = 0x00780078u, ones = 0x41804180u;
-    __device__ __forceinline__ CodeConst() { asm volatile("" : "+v"(mask), "+v"(ones)); }
+    uint32_t mul = 0x8008u, mask = 0x00780078u, ones = 0x41804180u;
+    __device__ __forceinline__ CodeConst() { asm volatile("" : "+v"(mul), "+v"(mask), "+v"(ones)); }
 };
 __device__ __forceinline__ u32x4 code_values(const CodeConst& c, uint32_t w) {
-    return u32x4{((w << 3) & c.mask) | c.ones, ((w >> 1) & c.mask) | c.ones, ((w >> 5) & c.mask) | c.ones,
-                 ((w >> 9) & c.mask) | c.ones};
-}
-
-// eight consecutive x in the order of code_values' elements: 0, 4, 1, 5, 2, 6, 3, 7
-__device__ __forceinline__ u32x4 code_order(const u32x4& v) {
-    return u32x4{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
-                 __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (__umul24((w >> (8 * i)) & 255u, c.mul) & c.mask) | c.ones;
+    return v;
 }
 
 // s plus the eight x of v
@@ -165,7 +162,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void gemm_w4_rows_kernel(
 #pragma unroll
                 for (int t = 0; t < W; ++t) {
                     const u32x4 v = xr.x[g][t];
-                    d = mma_step(code_order(v), code_values(cc, now.c[g][t]), d, bf16_t{});
+                    d = mma_step(v, code_values(cc, now.c[g][t]), d, bf16_t{});
                     xs = add_x(v, xs);
                 }
                 acc = __builtin_amdgcn_mfma_f32_16x16x4f32(settled(xs), corr, acc, 0, 0, 0);
@@ -267,18 +264,23 @@ __device__ __forceinline__ void load_rows(const bf16_t* x, int m0, int M, int K,
     }
 }
 
-// One 128-deep piece: acc[a][b] += rows 32 a of x (LDS at xs, first row r0) times columns 32 b.
+// One 128-deep piece: acc[a][b] += rows 32 a of x (LDS at xs, first row r0) times columns 32 b.  The
+// fp32 operation that takes the zero points away has room for two depths, a lane half each: the two
+// halves' sums of one group, or the whole sums of two.
 template <int G, int MB, int NB>
 __device__ __forceinline__ void mul_piece(const uint8_t* xs, int r0, const typename W4Cols<G, NB>::Codes& p,
                                           const CodeConst& cc, f32x16 (&acc)[MB][NB]) {
     constexpr int NG = 128 / G, S = G / 16;
     const int lr = threadIdx.x & 31, hg = (threadIdx.x & 63) >> 5;
+    float sum[MB], corr[NB], sum0[MB], corr0[NB];   // (of the group, of the one before)
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         f32x16 d[MB][NB];
-        float sum[MB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) corr0[b] = g ? corr[b] : 0.f;
 #pragma unroll
         for (int a = 0; a < MB; ++a) {
+            sum0[a] = g ? sum[a] : 0.f;
             sum[a] = 0.f;
 #pragma unroll
             for (int b = 0; b < NB; ++b)
@@ -295,21 +297,31 @@ __device__ __forceinline__ void mul_piece(const uint8_t* xs, int r0, const typen
                 const int r = r0 + 32 * a + lr;
                 const u32x4 v = ld16(xs + r * 256 + ((g * (G / 8) + hg * S + t) ^ (r & 15)) * 16);
                 sum[a] = add_x(v, sum[a]);
-                const u32x4 xf = code_order(v);
 #pragma unroll
-                for (int b = 0; b < NB; ++b) d[a][b] = mma32(xf, cf[b], d[a][b]);
+                for (int b = 0; b < NB; ++b) d[a][b] = mma32(v, cf[b], d[a][b]);
             }
         }
 #pragma unroll
-        for (int a = 0; a < MB; ++a) sum[a] = settled(sum[a]);
-#pragma unroll
         for (int b = 0; b < NB; ++b) {
             const Scale sc(p.s[b][g]);
+            corr[b] = sc.corr;
 #pragma unroll
-            for (int a = 0; a < MB; ++a) {
-                acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(sum[a], sc.corr, acc[a][b], 0, 0, 0);
+            for (int a = 0; a < MB; ++a)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[a][b][i] = fmaf(sc.scale, d[a][b][i], acc[a][b][i]);
+        }
+        if (NG > 1 && g % 2 == 0) continue;
+#pragma unroll
+        for (int a = 0; a < MB; ++a) {
+            float z = settled(sum[a]);
+            if constexpr (NG > 1) {
+                const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum0[a]), __float_as_uint(z), false, false);
+                z = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float take = NG > 1 && hg == 0 ? corr0[b] : corr[b];
+                acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(z, take, acc[a][b], 0, 0, 0);
             }
         }
     }
@@ -398,9 +410,8 @@ __global__ __launch_bounds__(64 * kDecodeWaves, 2) void gemm_w4_decode_kernel(
                 for (int a = 0; a < MB; ++a) {
                     const u32x4 v = ld16(xs + (32 * a + lr) * 128 + ((g * (GH / 8) + hg * S + t) ^ ((lr >> 1) & 7)) * 16);
                     sum[a] = add_x(v, sum[a]);
-                    const u32x4 xf = code_order(v);
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) d[a][b] = mma32(xf, cf[b], d[a][b]);
+    #pragma unroll
+                    for (int b = 0; b < NB; ++b) d[a][b] = mma32(v, cf[b], d[a][b]);
                 }
             }
             if (G <= 64 || half == 1) {
