@@ -89,7 +89,7 @@ __device__ __forceinline__ void shrink_rows(const LoraArgs& a, const int32_t* ta
     }
 }
 
-// Shrink unit u (a workgroup of 4 waves): rank-rows j0 .. j0 + 3 of group g,
+// Shrink unit u (4 waves, this the wave-th of them): rank-rows j0 .. j0 + 3 of group g,
 // for the group's rows first .. first + kShrinkTokensPerUnit - 1.  Its index
 // entry (8 words): [0] group, [1] j0 | first << 8, [2] slot, [3] rank | rows
 // << 8, [4..7] the unit's rows (the last repeated).  RES reads the resolved
@@ -97,7 +97,7 @@ __device__ __forceinline__ void shrink_rows(const LoraArgs& a, const int32_t* ta
 // dependent loads when the index is read from host memory; otherwise the
 // group's table entries are read.
 template <typename E, bool RES = false>
-__device__ __forceinline__ void bgmv_shrink_unit(const LoraArgs& a, int u, int lp, float* v) {
+__device__ __forceinline__ void bgmv_shrink_unit(const LoraArgs& a, int u, int lp, float* v, int wave) {
     constexpr int TB = kShrinkTokensPerPass;
     static_assert(TB == 4 && kShrinkTokensPerUnit == TB, "one pass of 1 to 4 rows");
     const int lane = threadIdx.x & 63;
@@ -107,14 +107,14 @@ __device__ __forceinline__ void bgmv_shrink_unit(const LoraArgs& a, int u, int l
     if constexpr (RES) {
         const int4 h = reinterpret_cast<const int4*>(a.su)[2 * u];
         rr = reinterpret_cast<const int4*>(a.su)[2 * u + 1];
-        j = (h.y & 255) + (threadIdx.x >> 6);
+        j = (h.y & 255) + wave;
         slot = h.z;
         r = h.w & 255;
         cnt = h.w >> 8;
     } else {
         const int2 unit = reinterpret_cast<const int2*>(a.su)[4 * u];
         const int g = unit.x;
-        j = (unit.y & 255) + (threadIdx.x >> 6);
+        j = (unit.y & 255) + wave;
         first = unit.y >> 8;
         slot = a.g_slot[g];
         r = a.g_rank[g];
@@ -144,6 +144,10 @@ __device__ __forceinline__ void bgmv_shrink_unit(const LoraArgs& a, int u, int l
             default: shrink_rows<E, 4>(a, tab, j, row, lane, v); break;
         }
     }
+}
+template <typename E, bool RES = false>
+__device__ __forceinline__ void bgmv_shrink_unit(const LoraArgs& a, int u, int lp, float* v) {
+    bgmv_shrink_unit<E, RES>(a, u, lp, v, threadIdx.x >> 6);
 }
 template <typename E, bool RES = false>
 __device__ __forceinline__ void bgmv_shrink_unit(const LoraArgs& a, int u) {

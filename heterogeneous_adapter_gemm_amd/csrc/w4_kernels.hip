@@ -12,8 +12,11 @@
 // A lane of a matrix operation has a row of x (a row of codes) and its share of
 // a group's k, consecutive ones: group / 4 of them where four lanes share a row
 // (16-row operations), group / 2 where two do (32-row operations).
+#include "bgmv_device.h"
 #include "common.h"
 #include "internal.h"
+
+#include <type_traits>
 
 namespace hagemm {
 namespace {
@@ -83,13 +86,20 @@ __device__ __forceinline__ void ld_words(const uint8_t* p, uint32_t (&o)[W]) {
     }
 }
 
-__device__ __forceinline__ void put(bf16_t* y, float* ybase, const int32_t* row_slot, int m, int n, int N, float v) {
-    const int64_t off = (int64_t)m * N + n;
-    if (row_slot != nullptr && row_slot[m] >= 0)
-        ybase[off] = v;
-    else
-        y[off].bits = (uint16_t)f32_to_bf16(v);
-}
+// y[m][n] = v; of a row with an adapter (its bit in raw_mask, or row_slot where that is 0) to ybase, unrounded
+struct Out {
+    bf16_t* y;
+    float* ybase;
+    const int32_t* row_slot;
+    uint64_t raw_mask;
+    __device__ __forceinline__ void put(int m, int n, int N, float v) const {
+        const int64_t off = (int64_t)m * N + n;
+        if (raw_mask ? m < 64 && raw_mask >> m & 1 : row_slot != nullptr && row_slot[m] >= 0)
+            ybase[off] = v;
+        else
+            y[off].bits = (uint16_t)f32_to_bf16(v);
+    }
+};
 
 // ---------------------------------------------------------------- up to 16 rows
 
@@ -99,12 +109,11 @@ __device__ __forceinline__ void put(bf16_t* y, float* ybase, const int32_t* row_
 constexpr int kRowWaves = 8;
 
 template <int G>
-__global__ __launch_bounds__(64 * kRowWaves) void gemm_w4_rows_kernel(
-    const bf16_t* __restrict__ x, const uint8_t* __restrict__ q, const uint32_t* __restrict__ sz,
-    bf16_t* __restrict__ y, int M, int N, int K, const int32_t* __restrict__ row_slot, float* __restrict__ ybase) {
+__device__ __forceinline__ void rows_tile(const bf16_t* __restrict__ x, const uint8_t* __restrict__ q,
+                                          const uint32_t* __restrict__ sz, const Out& out, int M, int N, int K, int bx) {
     __shared__ float part[kRowWaves][4][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, lg = lane >> 4;
-    const int n0 = blockIdx.x * 16, n = min(n0 + li, N - 1);
+    const int n0 = bx * 16, n = min(n0 + li, N - 1);
     constexpr int NG = 128 / G, W = G / 32;   // groups of a piece; words (and steps) of a group a lane
     const uint8_t* qn = q + (int64_t)n * (K / 2) + lg * (G / 8);
     const uint32_t* sn = sz + (int64_t)n * (K / G);
@@ -180,7 +189,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void gemm_w4_rows_kernel(
 #pragma unroll
         for (int w = 0; w < kRowWaves; ++w) v += part[w][wave][lane];
         const int m = 4 * lg + wave;
-        if (m < M && n0 + li < N) put(y, ybase, row_slot, m, n0 + li, N, v);
+        if (m < M && n0 + li < N) out.put(m, n0 + li, N, v);
     }
 }
 
@@ -337,9 +346,9 @@ __device__ __forceinline__ int row32(int i) { return 8 * (i / 4) + 4 * ((threadI
 constexpr int kDecodeWaves = 8;
 
 template <int G, int MB, int NB>
-__global__ __launch_bounds__(64 * kDecodeWaves, 2) void gemm_w4_decode_kernel(
-    const bf16_t* __restrict__ x, const uint8_t* __restrict__ q, const uint32_t* __restrict__ sz, bf16_t* __restrict__ y,
-    int M, int N, int K, const int32_t* __restrict__ row_slot, float* __restrict__ ybase) {
+__device__ __forceinline__ void decode_tile(const bf16_t* __restrict__ x, const uint8_t* __restrict__ q,
+                                            const uint32_t* __restrict__ sz, const Out& out, int M, int N, int K, int bx,
+                                            int by) {
     constexpr int kRows = 32 * MB, kStage = kRows * 128, W = kDecodeWaves;
     constexpr int GH = G < 64 ? G : 64, NG = 64 / GH, S = GH / 16;   // group's part of a half, parts of a half, steps of a part
     constexpr int kSums = MB * NB * 16 * 256;                       // a wave's sums
@@ -347,7 +356,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, 2) void gemm_w4_decode_kernel(
     __shared__ __attribute__((aligned(1024))) uint8_t lds[W * kLds];
     const int lane = threadIdx.x & 63, lr = lane & 31, hg = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = blockIdx.x * 32 * NB, m0 = blockIdx.y * kRows;
+    const int n0 = bx * 32 * NB, m0 = by * kRows;
     const CodeConst cc;
     uint8_t* place = lds + wave * 2 * kStage;
     const uint8_t* qn[NB];
@@ -432,7 +441,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, 2) void gemm_w4_decode_kernel(
     };
     const int n = (K / 128 - wave + W - 1) / W;   // pieces of this wave
     // (each workgroup begins at a piece of its own, so that they do not all read one slice of x at once)
-    const int shift = n > 0 ? (int)(blockIdx.x % n) : 0;
+    const int shift = n > 0 ? bx % n : 0;
     auto at = [&](int j) { return (wave + W * (j + shift < n ? j + shift : j + shift - n)) * 128; };
     Codes p[2];
     if (n > 0) issue(at(0), 0, p[0]);
@@ -465,7 +474,46 @@ __global__ __launch_bounds__(64 * kDecodeWaves, 2) void gemm_w4_decode_kernel(
 #pragma unroll
         for (int w = 0; w < W; ++w) v += part[w * (kSums / 4) + reg * 64 + lane];
         const int m = m0 + 32 * a + row32(i), c = n0 + 32 * b + lr;
-        if (m < M && c < N) put(y, ybase, row_slot, m, c, N, v);
+        if (m < M && c < N) out.put(m, c, N, v);
+    }
+}
+
+// One decode tile: rows (up to 16, up to 32, or blocks of 64) and columns by its kind
+enum DecodeKind { kRows16, kRows32, kRows64, kRows64Wide };
+template <int G, int KIND>
+__device__ __forceinline__ void any_tile(const bf16_t* __restrict__ x, const uint8_t* __restrict__ q,
+                                         const uint32_t* __restrict__ sz, const Out& out, int M, int N, int K, int bx, int by) {
+    if constexpr (KIND == kRows16) rows_tile<G>(x, q, sz, out, M, N, K, bx);
+    else if constexpr (KIND == kRows32) decode_tile<G, 1, 1>(x, q, sz, out, M, N, K, bx, by);
+    else if constexpr (KIND == kRows64) decode_tile<G, 2, 1>(x, q, sz, out, M, N, K, bx, by);
+    else decode_tile<G, 2, 2>(x, q, sz, out, M, N, K, bx, by);
+}
+constexpr int kTileThreads = 64 * kDecodeWaves;
+static_assert(kRowWaves == kDecodeWaves, "one workgroup size for every kind");
+constexpr int tile_columns(int kind) { return kind == kRows16 ? 16 : kind == kRows64Wide ? 64 : 32; }
+
+template <int G, int KIND>
+__global__ __launch_bounds__(kTileThreads, 2) void gemm_w4_decode_kernel(const bf16_t* __restrict__ x,
+                                                                         const uint8_t* __restrict__ q,
+                                                                         const uint32_t* __restrict__ sz, Out out, int M,
+                                                                         int N, int K) {
+    any_tile<G, KIND>(x, q, sz, out, M, N, K, blockIdx.x, blockIdx.y);
+}
+
+// Decode batches of up to 64 rows with adapters: the tiles, the BGMV shrink's units (two a
+// workgroup) and the copy of a plan's index in one launch.
+template <int G, int KIND>
+__global__ __launch_bounds__(kTileThreads, 2) void gemm_w4_shrink_kernel(
+    const bf16_t* __restrict__ x, const uint8_t* __restrict__ q, const uint32_t* __restrict__ sz, Out out, int M, int N, int K,
+    LoraArgs a, int n_gemm, int n_unit, const uint32_t* __restrict__ cp_src, uint32_t* __restrict__ cp_dst, int cp_n) {
+    const int b = blockIdx.x;
+    if (b < n_gemm) {
+        any_tile<G, KIND>(x, q, sz, out, M, N, K, b, 0);
+    } else if (b < n_gemm + n_unit) {
+        const int wave = threadIdx.x >> 6;
+        bgmv_shrink_unit<bf16_t, true>(a, 2 * (b - n_gemm) + wave / 4, a.lp_per_rank, a.v, wave % 4);
+    } else if (threadIdx.x < 256) {
+        copy_words(cp_src, cp_dst, cp_n, b - n_gemm - n_unit);
     }
 }
 
@@ -474,9 +522,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, 2) void gemm_w4_decode_kernel(
 // putting the codes in place and the sums of a group to scale.
 template <int G>
 __global__ __launch_bounds__(256, 2) void gemm_w4_long_kernel(const bf16_t* __restrict__ x, const uint8_t* __restrict__ q,
-                                                              const uint32_t* __restrict__ sz, bf16_t* __restrict__ y,
-                                                              int M, int N, int K, const int32_t* __restrict__ row_slot,
-                                                              float* __restrict__ ybase) {
+                                                              const uint32_t* __restrict__ sz, Out out, int M, int N, int K) {
     using Cols = W4Cols<G, 2>;
     __shared__ __attribute__((aligned(1024))) uint8_t lds0[128 * 256];
     __shared__ __attribute__((aligned(1024))) uint8_t lds1[128 * 256];
@@ -524,7 +570,7 @@ __global__ __launch_bounds__(256, 2) void gemm_w4_long_kernel(const bf16_t* __re
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int m = m0 + r0 + 32 * a + row32(i), c = n0 + 32 * b + (threadIdx.x & 31);
-                if (m < M && c < N) put(y, ybase, row_slot, m, c, N, acc[a][b][i]);
+                if (m < M && c < N) out.put(m, c, N, acc[a][b][i]);
             }
 }
 
@@ -536,21 +582,28 @@ bool gemm_w4_ok(int64_t M, int64_t N, int64_t K, int32_t group) {
     return M * K * 2 < INT32_MAX && N * K / 2 < INT32_MAX;
 }
 
-template <int G>
-static hipError_t gemm_w4(const bf16_t* x, const uint8_t* q, const uint32_t* sz, bf16_t* y, int M, int N, int K,
-                          const int32_t* row_slot, float* ybase, hipStream_t s) {
-    auto go = [&](auto kern, int64_t gx, int64_t gy, int threads) {
-        if (gx > INT32_MAX || gy > 65535) return hipErrorInvalidValue;
-        hipLaunchKernelGGL(kern, dim3((unsigned)gx, (unsigned)gy), dim3(threads), 0, s, x, q, sz, y, M, N, K, row_slot, ybase);
-        return hipGetLastError();
+// Up to 64 rows, and blocks of 64 of more; 64 rows wide where that still makes 160 workgroups (its
+// waves change half as many x to an operation; 64 rows 4096 -> 11008 18 us so, 21 us with 32 columns,
+// and 4096 -> 4096 12.3 us with 32 columns, 17 us with 64).
+static DecodeKind decode_kind(int64_t M, int64_t N) {
+    return M <= 16 ? kRows16 : M <= 32 ? kRows32 : N >= 64 * 160 ? kRows64Wide : kRows64;
+}
+static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// f(integral_constant group, integral_constant kind)
+template <typename F>
+static hipError_t with_kind(int32_t group, DecodeKind kind, F&& f) {
+    auto k = [&](auto g) {
+        switch (kind) {
+            case kRows16: return f(g, std::integral_constant<int, kRows16>{});
+            case kRows32: return f(g, std::integral_constant<int, kRows32>{});
+            case kRows64: return f(g, std::integral_constant<int, kRows64>{});
+            default: return f(g, std::integral_constant<int, kRows64Wide>{});
+        }
     };
-    auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-    if (M <= 16) return go(gemm_w4_rows_kernel<G>, cdiv(N, 16), 1, 64 * kRowWaves);
-    const int64_t tiles = cdiv(M, 128) * cdiv(N, 128);
-    if (M > 64 && tiles >= 128) return go(gemm_w4_long_kernel<G>, tiles, 1, 256);
-    if (M <= 32) return go(gemm_w4_decode_kernel<G, 1, 1>, cdiv(N, 32), 1, 64 * kDecodeWaves);
-    if (N >= 64 * 160) return go(gemm_w4_decode_kernel<G, 2, 2>, cdiv(N, 64), cdiv(M, 64), 64 * kDecodeWaves);
-    return go(gemm_w4_decode_kernel<G, 2, 1>, cdiv(N, 32), cdiv(M, 64), 64 * kDecodeWaves);
+    return group == 128  ? k(std::integral_constant<int, 128>{})
+           : group == 64 ? k(std::integral_constant<int, 64>{})
+                         : k(std::integral_constant<int, 32>{});
 }
 
 hipError_t launch_gemm_w4(const void* x, const void* q, const void* sz, int32_t group, void* y, int64_t M, int64_t N,
@@ -559,10 +612,41 @@ hipError_t launch_gemm_w4(const void* x, const void* q, const void* sz, int32_t 
     const bf16_t* xb = static_cast<const bf16_t*>(x);
     const uint8_t* qb = static_cast<const uint8_t*>(q);
     const uint32_t* zb = static_cast<const uint32_t*>(sz);
-    bf16_t* yb = static_cast<bf16_t*>(y);
-    if (group == 128) return gemm_w4<128>(xb, qb, zb, yb, (int)M, (int)N, (int)K, row_slot, ybase, s);
-    if (group == 64) return gemm_w4<64>(xb, qb, zb, yb, (int)M, (int)N, (int)K, row_slot, ybase, s);
-    return gemm_w4<32>(xb, qb, zb, yb, (int)M, (int)N, (int)K, row_slot, ybase, s);
+    const Out out{static_cast<bf16_t*>(y), ybase, row_slot, 0};
+    auto go = [&](auto kern, int64_t gx, int64_t gy, int threads) {
+        if (gx > INT32_MAX || gy > 65535) return hipErrorInvalidValue;
+        hipLaunchKernelGGL(kern, dim3((unsigned)gx, (unsigned)gy), dim3(threads), 0, s, xb, qb, zb, out, (int)M, (int)N, (int)K);
+        return hipGetLastError();
+    };
+    const int64_t tiles = cdiv(M, 128) * cdiv(N, 128);
+    if (M > 64 && tiles >= 128)
+        return group == 128  ? go(gemm_w4_long_kernel<128>, tiles, 1, 256)
+               : group == 64 ? go(gemm_w4_long_kernel<64>, tiles, 1, 256)
+                             : go(gemm_w4_long_kernel<32>, tiles, 1, 256);
+    const DecodeKind kind = decode_kind(M, N);
+    return with_kind(group, kind, [&](auto g, auto k) {
+        return go(gemm_w4_decode_kernel<g.value, k.value>, cdiv(N, tile_columns(kind)), cdiv(M, 64), kTileThreads);
+    });
+}
+
+bool gemm_w4_shrink_fits(int64_t M, int64_t N, int64_t K, int32_t group, int n_su) {
+    return M >= 1 && M <= 64 && n_su > 0 && n_su <= kW4ShrinkUnits && gemm_w4_ok(M, N, K, group);
+}
+
+hipError_t launch_gemm_w4_shrink(const void* x, const void* q, const void* sz, int32_t group, void* y, int64_t M, int64_t N,
+                                 int64_t K, const int32_t* row_slot, uint64_t raw_mask, float* ybase, const LoraArgs& a,
+                                 const void* cp_src, void* cp_dst, int64_t cp_n, hipStream_t s) {
+    if (!gemm_w4_shrink_fits(M, N, K, group, a.n_su) || cp_n < 0 || cp_n > INT32_MAX) return hipErrorInvalidValue;
+    const Out out{static_cast<bf16_t*>(y), ybase, row_slot, raw_mask};
+    const DecodeKind kind = decode_kind(M, N);
+    const int tn = (int)cdiv(N, tile_columns(kind)), nu = (a.n_su + 1) / 2, ncp = cp_n > 0 ? kCopyBlocks : 0;
+    return with_kind(group, kind, [&](auto g, auto k) {
+        hipLaunchKernelGGL((gemm_w4_shrink_kernel<g.value, k.value>), dim3((unsigned)(tn + nu + ncp)), dim3(kTileThreads), 0, s,
+                           static_cast<const bf16_t*>(x), static_cast<const uint8_t*>(q), static_cast<const uint32_t*>(sz), out,
+                           (int)M, (int)N, (int)K, a, tn, nu, static_cast<const uint32_t*>(cp_src),
+                           static_cast<uint32_t*>(cp_dst), (int)cp_n);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace hagemm
