@@ -186,8 +186,7 @@ hipError_t launch_gemm_w8(const void* x, const void* q, const float* scale, void
 bool gemm_w4_ok(int64_t M, int64_t N, int64_t K, int32_t group);
 hipError_t launch_gemm_w4(const void* x, const void* q, const void* sz, int32_t group, void* y, int64_t M, int64_t N,
                           int64_t K, const int32_t* row_slot, float* ybase, hipStream_t s);
-// 4-bit base for decode batches (M <= 64, 0 < a.n_su <= kW4ShrinkUnits): as launch_gemm_w8_shrink.
-constexpr int kW4ShrinkUnits = 512;
+// 4-bit base for decode batches (M <= 64, a.n_su > 0): as launch_gemm_w8_shrink.
 bool gemm_w4_shrink_fits(int64_t M, int64_t N, int64_t K, int32_t group, int n_su);
 hipError_t launch_gemm_w4_shrink(const void* x, const void* q, const void* sz, int32_t group, void* y, int64_t M, int64_t N,
                                  int64_t K, const int32_t* row_slot, uint64_t raw_mask, float* ybase, const LoraArgs& a,

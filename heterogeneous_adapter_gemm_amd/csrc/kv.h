@@ -40,11 +40,14 @@ constexpr int kKvPrefillRows = 128;      // query rows of a prefill segment
 // 256 CUs 16 (head_dim 64), 12 (128) or 8 (256).  A prefill worker is a workgroup of four, two a CU.
 constexpr int kKvPrefillWorkers = 512;
 constexpr int kv_workers(int head_dim) { return 1024 * (head_dim == 64 ? 4 : head_dim == 128 ? 3 : 2); }
-// An entry a worker, and two partial results of a row tile of fp32 sums and (m, l) each.
+// An entry a worker, and two partial results of a row tile of fp32 sums and (m, l) each; where
+// sequences of few and of many rows may meet in a batch, both kinds' side by side.
+constexpr int64_t kv_few_bytes(int head_dim) {
+    return (int64_t)kv_workers(head_dim) * (36 + 2 * kKvRowTile * (head_dim + 2) * 4);
+}
 constexpr int64_t kv_workspace_bytes(int head_dim, int group, int max_rows) {
-    const int64_t few = (int64_t)kv_workers(head_dim) * (36 + 2 * kKvRowTile * (head_dim + 2) * 4);
     const int64_t many = (int64_t)kKvPrefillWorkers * (36 + 2 * kKvPrefillRows * (head_dim + 2) * 4);
-    return (int64_t)max_rows * group <= kKvRowTile || few > many ? few : many;
+    return kv_few_bytes(head_dim) + ((int64_t)max_rows * group <= kKvRowTile ? 0 : many);
 }
 
 hipError_t launch_kv_append(int head_dim, const KvArgs& b, const KvAppendArgs& a, hipStream_t s);

@@ -864,8 +864,8 @@ __device__ __forceinline__ bf16_t* out_row(const KvArgs& b, const KvOut& w, int 
 // whole workgroup's piece is inside one segment its waves' sums meet in LDS, so that long
 // sequences leave a part a workgroup.  Bound by reading the cache once.
 template <int D, int SUB, bool SPLIT>
-__global__ __launch_bounds__(256, D == 256 ? 2 : 3) void kv_decode_kernel(KvArgs b, const bf16_t* q, int64_t q_stride,
-                                                                          KvOut w, float c, KvCut cut) {
+__device__ __forceinline__ void decode_piece(const KvArgs& b, const bf16_t* q, int64_t q_stride, const KvOut& w, float c,
+                                             const KvCut& cut, int wg) {
     using Wave = KvWave<D, SUB, SPLIT>;
     constexpr int NE = D / 16, RB = Wave::ROWS;
     constexpr int kStage = KvStage<D>::kBytes, kSums = RB * (D + 4) * 4;
@@ -879,7 +879,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 3) void kv_decode_kernel(KvArgs
     const int lane = threadIdx.x & 63, lg = lane >> 4, row = Wave::row();
     const bool first_col = Wave::col() == 0;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wg = blockIdx.x, worker = 4 * wg + wave;
+    const int worker = 4 * wg + wave;
     const KvPieces pieces(uniform64(line.before[256]), cut.workers);
     int64_t pos = pieces.at(min(worker, pieces.workers));
     const int64_t end = pieces.at(min(worker + 1, pieces.workers));
@@ -1214,8 +1214,8 @@ struct KvRows {
 };
 
 template <int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_prefill_kernel(KvArgs b, const bf16_t* q, int64_t q_stride,
-                                                                           KvOut w, float c, KvCut cut) {
+__device__ __forceinline__ void prefill_piece(const KvArgs& b, const bf16_t* q, int64_t q_stride, const KvOut& w, float c,
+                                              const KvCut& cut, int worker) {
     using Rows = KvRows<D>;
     constexpr int RB = kKvPrefillRows;
     __shared__ __attribute__((aligned(1024))) uint8_t stage0[Rows::kStage];
@@ -1225,7 +1225,6 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_prefill_kernel(KvArg
     kv_line(b, cut, line);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int worker = blockIdx.x;
     const KvPieces pieces(uniform64(line.before[256]), cut.workers);
     int64_t pos = pieces.at(min(worker, pieces.workers));
     const int64_t end = pieces.at(min(worker + 1, pieces.workers));
@@ -1360,7 +1359,7 @@ __device__ __forceinline__ KvSum sum_parts(const KvOut& w, const KvMerge& e, int
 // workers for the cut segments and takes its share: a row a wave at a time, or, where there are
 // fewer rows than workgroups, a row a workgroup.  The order of the sums is fixed.
 template <int D>
-__global__ __launch_bounds__(256) void kv_merge_kernel(KvArgs b, KvOut w, float c, int rb, int most_rows) {
+__device__ __forceinline__ void merge_list(const KvArgs& b, const KvOut& w, float c, int rb, int most_rows, int wg, int wgs) {
     constexpr int TPR = D / 4, PW = 256 / TPR, WW = 64 / TPR, kMost = kv_workers(D) / 256;
     __shared__ float sa[PW][D + 4], sm[PW], sl[PW];
     __shared__ int sums[4], list[kv_workers(D)];
@@ -1390,7 +1389,7 @@ __global__ __launch_bounds__(256) void kv_merge_kernel(KvArgs b, KvOut w, float 
     for (; mine; mine &= mine - 1) list[at++] = threadIdx.x * kMost + __ffs(mine) - 1;
     __syncthreads();
     const int items = total * most_rows;
-    const bool per_wave = items > (int)gridDim.x;
+    const bool per_wave = items > wgs;
     auto store = [&](const KvMerge& e, int r, int d0, const KvSum& s) {
         const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
         u32x2 o;
@@ -1399,7 +1398,7 @@ __global__ __launch_bounds__(256) void kv_merge_kernel(KvArgs b, KvOut w, float 
         *reinterpret_cast<u32x2*>(out_row<D>(b, w, e.r0, e.h, e.row0 + r) + d0) = o;
     };
     const int d0 = threadIdx.x % TPR * 4;
-    for (int item = per_wave ? 4 * blockIdx.x + wave : blockIdx.x; item < items; item += (per_wave ? 4 : 1) * gridDim.x) {
+    for (int item = per_wave ? 4 * wg + wave : wg; item < items; item += (per_wave ? 4 : 1) * wgs) {
         const int first = __builtin_amdgcn_readfirstlane(list[item / most_rows]);
         const KvMerge e = reinterpret_cast<const KvMerge*>(w.ws)[first];
         const int n0 = min(4 * e.inside0, e.last + 1) - first + e.inside1 - e.inside0;
@@ -1437,35 +1436,150 @@ __global__ __launch_bounds__(256) void kv_merge_kernel(KvArgs b, KvOut w, float 
     }
 }
 
+// The same for row tiles of many rows, sixteen rows of a worker's cut segment a workgroup.  Mostly a
+// segment has two or three parts and every thread sums its rows' own.  From 17 parts on the
+// workgroups of its second to sixteenth worker, which have no segment of their own to join, take a
+// row each, and its threads share the parts.
+template <int D>
+__device__ __forceinline__ void merge_tile(const KvArgs& b, const KvOut& w, float c, int rb, int worker, int chunk) {
+    constexpr int TPR = D / 4, PW = 256 / TPR, RY = 16 / PW;
+    __shared__ float sa[PW][D + 4], sm[PW], sl[PW];
+    const int* lasts = reinterpret_cast<const int*>(w.ws + (int64_t)w.workers * sizeof(KvMerge));
+    const int back = min((int)(threadIdx.x & 63), min(worker, 15));
+    const int last_back = lasts[worker - back];
+    const uint64_t mine = __ballot(back == 0 ? last_back >= 0 : last_back >= worker - back + 16);
+    if (mine == 0) return;
+    const int x = worker - __builtin_ctzll(mine);
+    const KvMerge e = reinterpret_cast<const KvMerge*>(w.ws)[x];
+    const int n = e.last + 1 - x;
+    const int d0 = threadIdx.x % TPR * 4, pw = threadIdx.x / TPR;
+    auto store = [&](int r, const KvSum& s) {
+        const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
+        *reinterpret_cast<u32x2*>(out_row<D>(b, w, e.r0, e.h, e.row0 + r) + d0) =
+            u32x2{pack2(s.acc[0] * inv, s.acc[1] * inv), pack2(s.acc[2] * inv, s.acc[3] * inv)};
+    };
+    if (n > 16) {
+        const int r = 16 * chunk + worker - x;
+        if (r >= e.rows) return;
+        KvSum s = sum_parts<D>(w, e, x, n, rb, r, d0, pw, PW, c);
+        *reinterpret_cast<f32x4*>(&sa[pw][d0]) = s.acc;
+        if (d0 == 0) {
+            sm[pw] = s.m;
+            sl[pw] = s.l;
+        }
+        __syncthreads();
+        if (pw == 0) {
+#pragma unroll
+            for (int i = 1; i < PW; ++i) s.add(sm[i], sl[i], *reinterpret_cast<const f32x4*>(&sa[i][d0]), c);
+            store(r, s);
+        }
+        return;
+    }
+    const int r0 = 16 * chunk + pw;
+    KvSum s[RY];
+#pragma unroll
+    for (int y = 0; y < RY; ++y) s[y] = KvSum{-INFINITY, 0.f, f32x4{0.f, 0.f, 0.f, 0.f}};
+    for (int p = 0; p < n; p += 2) {
+        f32x4 v[2][RY];
+        float mp[2][RY], lp[2][RY];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int y = 0; y < RY; ++y) {
+                const int k = min(p + i, n - 1), slot = 2 * (x + k) + (k == 0), r = min(r0 + y * PW, e.rows - 1);
+                const float* ml = part_ml<D>(w, rb, slot, r);
+                v[i][y] = *reinterpret_cast<const f32x4*>(part_row<D>(w, rb, slot, r) + d0);
+                mp[i][y] = ml[0];
+                lp[i][y] = ml[1];
+            }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (p + i < n)
+#pragma unroll
+                for (int y = 0; y < RY; ++y) s[y].add(mp[i][y], lp[i][y], v[i][y], c);
+    }
+#pragma unroll
+    for (int y = 0; y < RY; ++y)
+        if (r0 + y * PW < e.rows) store(r0 + y * PW, s[y]);
+}
+
+// ---------------------------------------------------------------- attention: kernels
+
+template <int D, int SUB, bool SPLIT>
+__global__ __launch_bounds__(256, D == 256 ? 2 : 3) void kv_decode_kernel(KvArgs b, const bf16_t* q, int64_t q_stride,
+                                                                          KvOut w, float c, KvCut cut) {
+    decode_piece<D, SUB, SPLIT>(b, q, q_stride, w, c, cut, blockIdx.x);
+}
+
+template <int D>
+__global__ __launch_bounds__(256) void kv_merge_kernel(KvArgs b, KvOut w, float c, int rb, int most_rows) {
+    merge_list<D>(b, w, c, rb, most_rows, blockIdx.x, gridDim.x);
+}
+
+// Batches in which sequences of few and of many rows may meet: the pieces of many rows, then those of
+// few, in one launch, and then both kinds' sums.  (In turn, the few ones leave places to the others
+// unevenly: 512 pieces of many rows alone took 190 us so, 112 us this way.)
+struct KvBoth {
+    KvOut few, many;
+    KvCut few_cut, many_cut;
+};
+
+template <int D>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_mixed_kernel(KvArgs b, const bf16_t* q, int64_t q_stride, float c,
+                                                                         KvBoth k) {
+    const int nm = k.many.workers, i = blockIdx.x;
+    if (i < nm) prefill_piece<D>(b, q, q_stride, k.many, c, k.many_cut, i);
+    else decode_piece<D, 1, false>(b, q, q_stride, k.few, c, k.few_cut, i - nm);
+}
+
+constexpr int kTileChunks = kKvPrefillRows / 16;
+template <int D>
+__global__ __launch_bounds__(256) void kv_mixed_merge_kernel(KvArgs b, float c, KvBoth k) {
+    const int nm = k.many.workers * kTileChunks, i = blockIdx.x;
+    if (i < nm) merge_tile<D>(b, k.many, c, kKvPrefillRows, i / kTileChunks, i % kTileChunks);
+    else merge_list<D>(b, k.few, c, kKvRowTile, kKvRowTile, i - nm, gridDim.x - nm);
+}
+
 template <int D>
 hipError_t attention(const KvArgs& b, const bf16_t* q, int64_t q_stride, bf16_t* out, int64_t out_stride, float scale,
                      int32_t max_rows, void* workspace, hipStream_t s) {
     const float c = scale * 1.44269504088896341f;
     const int64_t rows = (int64_t)b.n_rows * b.group, most = (int64_t)max_rows * b.group;
-    auto go = [&](int rb_shift, int cls, int workers, int per_block, auto kern) {
+    auto pairs = [&](int rb_shift) { return ((rows >> rb_shift) + b.n_seqs) * b.kv_heads; };
+    auto share = [&](int rb_shift, int workers, int per_block) {
         // no more workers than steps there can be
-        const int64_t pairs = ((rows >> rb_shift) + b.n_seqs) * b.kv_heads;
-        const int64_t steps = std::max(1, (b.max_blocks + 1) / 2);
-        if (pairs < workers) workers = (int)std::min<int64_t>(workers, pairs * steps);
-        workers = (workers + 3) / 4 * 4;
-        const KvOut w{out, out_stride, static_cast<uint8_t*>(workspace), workers};
-        hipLaunchKernelGGL(kern, dim3(workers / per_block), dim3(256), 0, s, b, q, q_stride, w, c,
-                           KvCut{rb_shift, cls, workers});
+        const int64_t n = pairs(rb_shift), steps = std::max(1, (b.max_blocks + 1) / 2);
+        if (n < workers) workers = (int)std::min<int64_t>(workers, n * steps);
+        return (workers + per_block - 1) / per_block * per_block;
+    };
+    auto merge_grid = [&](int rb_shift, int workers, int most_rows) {
+        return (int)std::min<int64_t>(std::min<int64_t>(pairs(rb_shift), workers) * most_rows, 1024);
+    };
+    auto go = [&](int rb_shift, auto kern) {
+        const KvOut w{out, out_stride, static_cast<uint8_t*>(workspace), share(rb_shift, kv_workers(D), 4)};
+        hipLaunchKernelGGL(kern, dim3(w.workers / 4), dim3(256), 0, s, b, q, q_stride, w, c,
+                           KvCut{rb_shift, kKvAll, w.workers});
         const int most_rows = (int)std::min<int64_t>(1 << rb_shift, std::max<int64_t>(most, 1));
-        const int grid = (int)std::min<int64_t>(std::min<int64_t>(pairs, workers) * most_rows, 1024);
-        hipLaunchKernelGGL(kv_merge_kernel<D>, dim3(grid), dim3(256), 0, s, b, w, c, 1 << rb_shift, most_rows);
+        hipLaunchKernelGGL(kv_merge_kernel<D>, dim3(merge_grid(rb_shift, w.workers, most_rows)), dim3(256), 0, s, b, w, c,
+                           1 << rb_shift, most_rows);
         return hipGetLastError();
     };
     static_assert(kKvRowTile == 16 && kKvPrefillRows == 128, "row tiles");
     // few rows: as many columns of a matrix operation a row as there are
-    const int n = kv_workers(D);
-    if (most <= 1) return go(0, kKvAll, n, 4, kv_decode_kernel<D, 8, true>);
-    if (most <= 2) return go(1, kKvAll, n, 4, kv_decode_kernel<D, 4, true>);
-    if (most <= 4) return go(2, kKvAll, n, 4, kv_decode_kernel<D, 4, false>);
-    if (most <= 8) return go(3, kKvAll, n, 4, kv_decode_kernel<D, 2, false>);
-    if (most <= 16) return go(4, kKvAll, n, 4, kv_decode_kernel<D, 1, false>);
-    hipError_t e = go(4, kKvFew, n, 4, kv_decode_kernel<D, 1, false>);
-    return e != hipSuccess ? e : go(7, kKvMany, kKvPrefillWorkers, 1, kv_prefill_kernel<D>);
+    if (most <= 1) return go(0, kv_decode_kernel<D, 8, true>);
+    if (most <= 2) return go(1, kv_decode_kernel<D, 4, true>);
+    if (most <= 4) return go(2, kv_decode_kernel<D, 4, false>);
+    if (most <= 8) return go(3, kv_decode_kernel<D, 2, false>);
+    if (most <= 16) return go(4, kv_decode_kernel<D, 1, false>);
+    KvBoth k;
+    k.few = KvOut{out, out_stride, static_cast<uint8_t*>(workspace), share(4, kv_workers(D), 4)};
+    k.many = KvOut{out, out_stride, k.few.ws + kv_few_bytes(D), share(7, kKvPrefillWorkers, 4)};
+    k.few_cut = KvCut{4, kKvFew, k.few.workers};
+    k.many_cut = KvCut{7, kKvMany, k.many.workers};
+    hipLaunchKernelGGL(kv_mixed_kernel<D>, dim3(k.few.workers / 4 + k.many.workers), dim3(256), 0, s, b, q, q_stride, c, k);
+    const int few_merge = merge_grid(4, k.few.workers, 16);
+    hipLaunchKernelGGL(kv_mixed_merge_kernel<D>, dim3(k.many.workers * kTileChunks + few_merge), dim3(256), 0, s, b, c, k);
+    return hipGetLastError();
 }
 
 }  // namespace
