@@ -99,6 +99,14 @@ struct Out {
         else
             y[off].bits = (uint16_t)f32_to_bf16(v);
     }
+    // columns n .. n + 3
+    __device__ __forceinline__ void put4(int m, int n, int N, const f32x4& v) const {
+        const int64_t off = (int64_t)m * N + n;
+        if (raw_mask ? m < 64 && raw_mask >> m & 1 : row_slot != nullptr && row_slot[m] >= 0)
+            *reinterpret_cast<f32x4*>(ybase + off) = v;
+        else
+            *reinterpret_cast<u32x2*>(y + off) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    }
 };
 
 // ---------------------------------------------------------------- up to 16 rows
@@ -467,14 +475,15 @@ __device__ __forceinline__ void decode_tile(const bf16_t* __restrict__ x, const 
 #pragma unroll
             for (int i = 0; i < 16; ++i) part[wave * (kSums / 4) + ((a * NB + b) * 16 + i) * 64 + lane] = acc[a][b][i];
     __syncthreads();
+    // four columns of a row a thread (N is a multiple of four)
 #pragma unroll
-    for (int e = 0; e < MB * NB * 16 / W; ++e) {
-        const int reg = e * W + wave, i = reg & 15, a = reg / 16 / NB, b = reg / 16 % NB;
-        float v = 0.f;
+    for (int e = threadIdx.x; e < MB * NB * 256; e += 64 * W) {
+        const int reg = e >> 4, l4 = (e & 15) * 4, blk = reg >> 4, i = reg & 15;
+        f32x4 v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < W; ++w) v += part[w * (kSums / 4) + reg * 64 + lane];
-        const int m = m0 + 32 * a + row32(i), c = n0 + 32 * b + lr;
-        if (m < M && c < N) out.put(m, c, N, v);
+        for (int w = 0; w < W; ++w) v += *reinterpret_cast<const f32x4*>(part + w * (kSums / 4) + reg * 64 + l4);
+        const int m = m0 + 32 * (blk / NB) + 8 * (i / 4) + 4 * (l4 >> 5) + i % 4, c = n0 + 32 * (blk % NB) + (l4 & 31);
+        if (m < M && c < N) out.put4(m, c, N, v);
     }
 }
 
