@@ -39,6 +39,9 @@ int check_sizes(const lora_kv_batch* b) {
     if (b->n_seqs < 0 || b->n_seqs > (1 << 20) || b->n_rows < 0 || b->n_rows > (1 << 22) || b->max_rows < 0 ||
         b->max_blocks < 0 || b->max_blocks > (1 << 26) || b->reserved != 0)
         return set_error(LORA_EINVAL, "n_seqs, n_rows, max_rows or max_blocks out of range, or reserved not 0");
+    // (the kernels count a batch's rows of all heads in 32 bits)
+    if ((int64_t)b->n_rows * b->n_heads > (int64_t(1) << 30))
+        return set_error(LORA_EINVAL, "%d rows of %d heads: at most 2^30 together", b->n_rows, b->n_heads);
     return LORA_OK;
 }
 

@@ -427,6 +427,7 @@ int lora_linear_w4(lora_pool* pool, const lora_plan* plan, int32_t layer, int32_
  * are left out of the attention.
  *   head_dim     64, 128 or 256;  n_heads a multiple of n_kv_heads (query head h
  *                reads KV head h / (n_heads / n_kv_heads))
+ *   n_rows       at most 2^22, and n_rows * n_heads at most 2^30
  *   max_rows     the most rows of one sequence: chooses kernels and the
  *                workspace's size, never which rows are computed
  *   page_table   [n_seqs][max_blocks][pages per block], of one layer; entries

@@ -159,3 +159,14 @@ def test_oracle_attention_by_hand():
     assert np.allclose(out[0], 0.5) and np.allclose(out[1], 1.0)
     assert np.allclose(KV.attention(q, k, v, 1, 0.5, hidden=[0])[1], 1.5)
     assert not KV.attention(q, k[:1], v[:1], 1, 0.5)[0].any()       # two rows, one token: the first sees none
+
+
+def test_rows_of_all_heads_stay_in_32_bits():
+    """Row and tile numbers over all heads are 32-bit in the kernels: larger batches are refused."""
+    pool = host_pool()
+    big = dict(n_heads=1024, n_kv_heads=1, n_rows=1 << 20)
+    for b in (batch(**dict(big, n_rows=(1 << 20) + 1)), batch(**dict(big, n_heads=2048))):
+        refused(lambda: hg.lora_kv_append(pool.pool, b, rows(), stream=0), "2^30")
+        refused(lambda: hg.lora_kv_attention(pool.pool, b, FAKE, 1 << 20, FAKE, 1 << 20, 1.0, FAKE, 1 << 40, stream=0), "2^30")
+        refused(lambda: hg.lora_kv_workspace_bytes(b), "2^30")
+    assert hg.lora_kv_workspace_bytes(batch(**big)) > 0
