@@ -226,6 +226,29 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _on_gpu(stream, call, *tensors) -> None:
+    """call(stream) on the GPU that holds the tensors, whichever is current (addresses: on the current one)."""
+    dev = None
+    for t in tensors:
+        if isinstance(t, int) or t is None:
+            continue
+        d = t.get_device() if hasattr(t, "get_device") else -1
+        if d < 0 or (dev is not None and d != dev):
+            raise ValueError("the tensors must be on one GPU")
+        dev = d
+    if dev is None:
+        call(_stream(stream))
+        return
+    import torch
+    if stream is None:
+        stream = current_stream(dev)
+    if torch.cuda.current_device() == dev:
+        call(_stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            call(_stream(stream))
+
+
 class Pool:
     """Owns a ``lora_pool*``; keeps the descriptor's arrays alive."""
 
@@ -471,14 +494,15 @@ def lora_linear_fp8(pool: Pool, plan: Plan, layer: int, proj: int, x, w0_code, w
 
 
 def base_gemm_w4(x, w0_code, w0_scale, y, M: int, N: int, K: int, group: int, stream=None) -> None:
-    _check(library().base_gemm_w4(_addr(x), _addr(w0_code), _addr(w0_scale), _addr(y), M, N, K, group,
-                                  _stream(stream)), "base_gemm_w4")
+    _on_gpu(stream, lambda st: _check(library().base_gemm_w4(_addr(x), _addr(w0_code), _addr(w0_scale), _addr(y), M, N, K,
+                                                             group, st), "base_gemm_w4"), x, w0_code, w0_scale, y)
 
 
 def lora_linear_w4(pool: Pool, plan: Plan, layer: int, proj: int, x, w0_code, w0_scale, group: int, y,
                    stream=None) -> None:
-    _check(library().lora_linear_w4(pool.handle, plan.handle, layer, proj, _addr(x), _addr(w0_code),
-                                    _addr(w0_scale), group, _addr(y), _stream(stream)), "lora_linear_w4")
+    _on_gpu(stream, lambda st: _check(library().lora_linear_w4(pool.handle, plan.handle, layer, proj, _addr(x),
+                                                               _addr(w0_code), _addr(w0_scale), group, _addr(y), st),
+                                      "lora_linear_w4"), x, w0_code, w0_scale, y)
 
 
 def lora_kv_pages_per_block(pool: Pool, n_kv_heads: int, head_dim: int) -> int:

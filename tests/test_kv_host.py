@@ -170,3 +170,16 @@ def test_rows_of_all_heads_stay_in_32_bits():
         refused(lambda: hg.lora_kv_attention(pool.pool, b, FAKE, 1 << 20, FAKE, 1 << 20, 1.0, FAKE, 1 << 40, stream=0), "2^30")
         refused(lambda: hg.lora_kv_workspace_bytes(b), "2^30")
     assert hg.lora_kv_workspace_bytes(batch(**big)) > 0
+
+
+def test_w4_host_tensors_are_refused():
+    import numpy as np
+    import torch
+    host = torch.zeros(8, 128, dtype=torch.bfloat16)
+    pool = host_pool()
+    plan = pool.plan(token_slot=[-1])
+    for bad in (host, np.zeros((8, 128), np.float32)):
+        with pytest.raises(ValueError, match="one GPU"):
+            hg.base_gemm_w4(bad, FAKE, FAKE, FAKE, 8, 8, 128, 64, stream=0)
+        with pytest.raises(ValueError, match="one GPU"):
+            pool.linear_w4(plan, 0, 0, FAKE, FAKE, FAKE, 64, bad, stream=0)
