@@ -59,14 +59,14 @@ class KvBatch:
         self.device, self.index = row_start.device, row_start.get_device()
         self.pages_per_block = page_table.shape[2]
         self.n_rows = n_rows
-        self.dtype = torch.bfloat16
+        self.dtype, self.f32, self.cuda = torch.bfloat16, torch.float32, torch.cuda
         self.c = L.lora_kv_batch(n_heads, n_kv_heads, head_dim, n_seqs, n_rows, n_rows if max_rows is None else max_rows,
                                  page_table.shape[1], 0, row_start.data_ptr(), ctx_len.data_ptr(),
                                  page_table.data_ptr())
         self.heads = (n_heads, head_dim), (n_kv_heads, head_dim)
 
-    def rows(self, name: str, t, kv: bool) -> int:
-        """The row stride of t, checked to be this batch's rows of the query (or KV) heads."""
+    def rows(self, name: str, t, kv: bool):
+        """Address and row stride of t, checked to be this batch's rows of the query (or KV) heads."""
         heads, dim = self.heads[kv]
         if t.get_device() != self.index or t.dtype is not self.dtype:
             raise ValueError(f"{name} must be {self.dtype} on {self.device}")
@@ -79,7 +79,7 @@ class KvBatch:
             raise ValueError(f"{name}: shape {tuple(shape)}, not [rows, {heads}, {dim}] or [rows, {heads * dim}]")
         if shape[0] != self.n_rows or not inner:
             raise ValueError(f"{name}: {self.n_rows} rows of contiguous heads are needed")
-        return st[0] if self.n_rows > 1 else heads * dim
+        return t.data_ptr(), st[0] if self.n_rows > 1 else heads * dim
 
 
 class DevicePool:
@@ -210,45 +210,41 @@ class DevicePool:
         import torch
         return torch.empty(L.lora_kv_workspace_bytes(batch.c), dtype=torch.uint8, device=batch.device)
 
-    def _kv_call(self, batch: KvBatch, stream, call) -> None:
-        """call(stream) on the batch's GPU, whichever is current."""
-        import torch
+    def _kv_call(self, batch: KvBatch, stream, call, *args) -> None:
+        """call(pool, batch, *args, stream) on the batch's GPU, whichever is current."""
         if self.pages is None or batch.index != self.pages.get_device():
             raise ValueError(f"the batch is on {batch.device}, the pool on {None if self.pages is None else self.pages.device}")
-        need = self.kv_pages_per_block(batch.heads[1][0], batch.heads[1][1])
+        need = self.kv_pages_per_block(*batch.heads[1])
         if batch.pages_per_block != need:
             raise ValueError(f"page_table has {batch.pages_per_block} pages a block, {need} are needed")
         if stream is None:
             stream = L.current_stream(batch.index)
-        if torch.cuda.current_device() == batch.index:
-            call(stream)
+        cuda = batch.cuda
+        if cuda.current_device() == batch.index:
+            call(self.pool, batch.c, *args, stream)
         else:
-            with torch.cuda.device(batch.index):
-                call(stream)
+            with cuda.device(batch.index):
+                call(self.pool, batch.c, *args, stream)
 
     def kv_append(self, batch: KvBatch, k, v, q=None, q_out=None, k_out=None, v_out=None, cos_sin=None,
                   interleaved: bool = False, stream=None) -> None:
         """Append the rows' keys and values to their pages; q, k turned by cos_sin [positions, rot_dim]."""
-        import torch
-        rows = batch.rows
-        r = L.lora_kv_rows(k.data_ptr(), v.data_ptr())
-        r.k_stride, r.v_stride = rows("k", k, True), rows("v", v, True)
-        if q is not None:
-            r.q, r.q_stride = q.data_ptr(), rows("q", q, False)
-        if q_out is not None:
-            r.q_out, r.q_out_stride = q_out.data_ptr(), rows("q_out", q_out, False)
-        if k_out is not None:
-            r.k_out, r.k_out_stride = k_out.data_ptr(), rows("k_out", k_out, True)
-        if v_out is not None:
-            r.v_out, r.v_out_stride = v_out.data_ptr(), rows("v_out", v_out, True)
+        rows, none = batch.rows, (None, 0)
+        kp, ks = rows("k", k, True)
+        vp, vs = rows("v", v, True)
+        qp, qs = none if q is None else rows("q", q, False)
+        tp, ts = none if q_out is None else rows("q_out", q_out, False)
+        kop, kos = none if k_out is None else rows("k_out", k_out, True)
+        vop, vos = none if v_out is None else rows("v_out", v_out, True)
+        r = L.lora_kv_rows(kp, vp, qp, tp, kop, vop, ks, vs, qs, ts, kos, vos)
         pos = rot = 0
         if cos_sin is not None:
-            if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or \
+            if cos_sin.dtype is not batch.f32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or \
                     cos_sin.get_device() != batch.index:
                 raise ValueError("cos_sin must be a contiguous float32 [positions, rot_dim] tensor on the batch's device")
             pos, rot = cos_sin.shape
-        self._kv_call(batch, stream,
-                      lambda st: L.lora_kv_append(self.pool, batch.c, r, cos_sin, rot, pos, interleaved, st))
+            cos_sin = cos_sin.data_ptr()
+        self._kv_call(batch, stream, L.lora_kv_append, r, cos_sin, rot, pos, interleaved)
 
     def kv_attention(self, batch: KvBatch, q, out, scale: Optional[float] = None, workspace=None, stream=None) -> None:
         """Attention of the batch's rows (q already turned) over the pages; scale None: head_dim ** -0.5."""
@@ -256,12 +252,11 @@ class DevicePool:
             raise ValueError("kv_attention needs a workspace (kv_workspace)")
         if workspace.get_device() != batch.index or not workspace.is_contiguous():
             raise ValueError("the workspace must be contiguous and on the batch's device")
-        qs, os_ = batch.rows("q", q, False), batch.rows("out", out, False)
+        (qp, qs), (op, os_) = batch.rows("q", q, False), batch.rows("out", out, False)
         if scale is None:
             scale = batch.heads[0][1] ** -0.5
         size = workspace.numel() * workspace.element_size()
-        self._kv_call(batch, stream,
-                      lambda st: L.lora_kv_attention(self.pool, batch.c, q, qs, out, os_, scale, workspace, size, st))
+        self._kv_call(batch, stream, L.lora_kv_attention, qp, qs, op, os_, scale, workspace.data_ptr(), size)
 
     def linear_decode(self, layer: int, proj: int, x, w0, y, token_slot, stream=None) -> None:
         L.lora_linear_decode(self.pool, layer, proj, x, w0, y, token_slot, stream)
