@@ -282,65 +282,64 @@ __device__ __forceinline__ void load_rows(const bf16_t* x, int m0, int M, int K,
     }
 }
 
-// One 128-deep piece: acc[a][b] += rows 32 a of x (LDS at xs, first row r0) times columns 32 b.  The
-// fp32 operation that takes the zero points away has room for two depths, a lane half each: the two
-// halves' sums of one group, or the whole sums of two.
-template <int G, int MB, int NB>
-__device__ __forceinline__ void mul_piece(const uint8_t* xs, int r0, const typename W4Cols<G, NB>::Codes& p,
-                                          const CodeConst& cc, f32x16 (&acc)[MB][NB]) {
+// What a piece takes away for its zero points, one fp32 matrix operation for a pair of groups: it has
+// room for two depths, a lane half each, the two halves' sums of one group or the whole sums of two.
+template <int G, int NB>
+struct Taken {
+    static constexpr int NP = G == 32 ? 2 : 1;
+    float sum[NP], corr[NP][NB];   // of this lane's row and group; of its column and group
+};
+
+// One 128-deep piece of a wave's 64 x 32 NB: acc[a][b] += rows row[a] of x (LDS at xs) times columns 32 b,
+// but for the zero points; out: those of rows row[0].
+template <int G, int NB>
+__device__ __forceinline__ void mul_piece(const uint8_t* xs, const int (&row)[2], const typename W4Cols<G, NB>::Codes& p,
+                                          const CodeConst& cc, f32x16 (&acc)[2][NB], Taken<G, NB>& out) {
     constexpr int NG = 128 / G, S = G / 16;
-    const int lr = threadIdx.x & 31, hg = (threadIdx.x & 63) >> 5;
-    float sum[MB], corr[NB], sum0[MB], corr0[NB];   // (of the group, of the one before)
+    const int hg = (threadIdx.x & 63) >> 5;
+    float sum0 = 0.f, corr0[NB];   // (of the group before)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) corr0[b] = 0.f;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        f32x16 d[MB][NB];
+        f32x16 d[2][NB];
+        float sum = 0.f;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) corr0[b] = g ? corr[b] : 0.f;
-#pragma unroll
-        for (int a = 0; a < MB; ++a) {
-            sum0[a] = g ? sum[a] : 0.f;
-            sum[a] = 0.f;
+        for (int a = 0; a < 2; ++a)
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) d[a][b][i] = 0.f;
-        }
 #pragma unroll
         for (int t = 0; t < S; ++t) {
             u32x4 cf[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) cf[b] = code_values(cc, p.c[b][g][t]);
 #pragma unroll
-            for (int a = 0; a < MB; ++a) {
-                const int r = r0 + 32 * a + lr;
-                const u32x4 v = ld16(xs + r * 256 + ((g * (G / 8) + hg * S + t) ^ (r & 15)) * 16);
-                sum[a] = add_x(v, sum[a]);
+            for (int a = 0; a < 2; ++a) {
+                const u32x4 v = ld16(xs + row[a] * 256 + ((g * (G / 8) + hg * S + t) ^ (row[a] & 15)) * 16);
+                if (a == 0) sum = add_x(v, sum);
 #pragma unroll
                 for (int b = 0; b < NB; ++b) d[a][b] = mma32(v, cf[b], d[a][b]);
             }
         }
+        sum = settled(sum);
+        if (NG > 1 && g % 2) {
+            const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum0), __float_as_uint(sum), false, false);
+            out.sum[g / 2] = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+        } else if (NG == 1) {
+            out.sum[0] = sum;
+        }
+        sum0 = sum;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const Scale sc(p.s[b][g]);
-            corr[b] = sc.corr;
+            out.corr[g / 2][b] = NG > 1 && hg == 0 ? corr0[b] : sc.corr;
+            corr0[b] = sc.corr;
 #pragma unroll
-            for (int a = 0; a < MB; ++a)
+            for (int a = 0; a < 2; ++a)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[a][b][i] = fmaf(sc.scale, d[a][b][i], acc[a][b][i]);
-        }
-        if (NG > 1 && g % 2 == 0) continue;
-#pragma unroll
-        for (int a = 0; a < MB; ++a) {
-            float z = settled(sum[a]);
-            if constexpr (NG > 1) {
-                const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum0[a]), __float_as_uint(z), false, false);
-                z = __uint_as_float(h[0]) + __uint_as_float(h[1]);
-            }
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const float take = NG > 1 && hg == 0 ? corr0[b] : corr[b];
-                acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(z, take, acc[a][b], 0, 0, 0);
-            }
         }
     }
 }
@@ -544,6 +543,7 @@ __global__ __launch_bounds__(256, 2) void gemm_w4_long_kernel(const bf16_t* __re
     using Cols = W4Cols<G, 2>;
     __shared__ __attribute__((aligned(1024))) uint8_t lds0[128 * 256];
     __shared__ __attribute__((aligned(1024))) uint8_t lds1[128 * 256];
+    __shared__ float zs[2][4][Taken<G, 2>::NP][64];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row_blocks = (M + 127) / 128, col_blocks = (N + 127) / 128;
     const int lid = xcd_logical(blockIdx.x, gridDim.x);
@@ -551,7 +551,9 @@ __global__ __launch_bounds__(256, 2) void gemm_w4_long_kernel(const bf16_t* __re
     // of a block of codes: so the tiles that run at once share most of either)
     const int strip = lid / (4 * col_blocks), in = lid - strip * 4 * col_blocks, high = min(4, row_blocks - 4 * strip);
     const int m0 = (4 * strip + in % high) * 128, n0 = (in / high) * 128 + (wave & 1) * 64;
-    const int r0 = (wave >> 1) * 64;
+    // two waves share 64 rows: either sums the x of the half that it calls its first
+    const int half = 32 * (wave & 1), r0 = (wave >> 1) * 64 + half, r1 = (wave >> 1) * 64 + (half ^ 32);
+    const int lane = threadIdx.x & 63, row[2] = {r0 + (lane & 31), r1 + (lane & 31)};
     const Cols cols(q, sz, n0, N, K);
     const CodeConst cc;
     f32x16 acc[2][2];
@@ -567,6 +569,19 @@ __global__ __launch_bounds__(256, 2) void gemm_w4_long_kernel(const bf16_t* __re
         load_rows(x, m0, M, K, j * 128, to, 32 * wave, 8);
         cols.load(j * 128, c);
     };
+    // the zero points of the piece before, its sums now there from both waves
+    Taken<G, 2> taken;
+    auto take = [&](int u) {
+#pragma unroll
+        for (int i = 0; i < taken.NP; ++i) {
+            const float other = zs[u][wave ^ 1][i][lane];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                acc[0][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(taken.sum[i], taken.corr[i][b], acc[0][b], 0, 0, 0);
+                acc[1][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(other, taken.corr[i][b], acc[1][b], 0, 0, 0);
+            }
+        }
+    };
     issue(0, lds0, p[0]);
 #pragma unroll 1
     for (int j = 0; j < n; j += 2) {
@@ -574,20 +589,27 @@ __global__ __launch_bounds__(256, 2) void gemm_w4_long_kernel(const bf16_t* __re
         for (int u = 0; u < 2; ++u) {
             if (j + u >= n) break;
             wait_vmcnt<0>();
-            landed();
+            wait_lgkm0();
             __builtin_amdgcn_s_barrier();   // every wave's rows are there, and the other place is read
             landed();
             if (j + u + 1 < n) issue(j + u + 1, u ? lds0 : lds1, p[1 - u]);
-            mul_piece<G, 2, 2>(u ? lds1 : lds0, r0, p[u], cc, acc);
+            if (j + u > 0) take(1 - u);
+            mul_piece<G, 2>(u ? lds1 : lds0, row, p[u], cc, acc, taken);
+#pragma unroll
+            for (int i = 0; i < taken.NP; ++i) zs[u][wave][i][lane] = taken.sum[i];
         }
     }
+    wait_lgkm0();
+    __builtin_amdgcn_s_barrier();
+    landed();
+    take((n - 1) & 1);
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const int m = m0 + r0 + 32 * a + row32(i), c = n0 + 32 * b + (threadIdx.x & 31);
+                const int m = m0 + (a ? r1 : r0) + row32(i), c = n0 + 32 * b + (threadIdx.x & 31);
                 if (m < M && c < N) out.put(m, c, N, acc[a][b][i]);
             }
 }
