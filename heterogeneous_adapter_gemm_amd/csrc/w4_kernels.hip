@@ -532,35 +532,28 @@ __global__ __launch_bounds__(kTileThreads, 2) void gemm_w4_shrink_kernel(
     }
 }
 
-// Long batches: 128 x 128 of y a workgroup, 64 x 64 a wave; the 128-deep pieces of x go to LDS
+// Long batches: 128 x 64 NB of y a workgroup, 64 x 32 NB a wave; the 128-deep pieces of x go to LDS
 // once for the four waves, one piece ahead.  Bound by the vector units and the matrix cores, which
-// share their issue: of 350 instructions for a piece of 64 x 64 128 put codes in place, 128 scale two
-// groups' sums, 64 sum x, beside 36 matrix operations.  Measured on MI355X: 2,961 x 4096 x 4096 in groups of
-// 64 150 us back to back, 0.66 PFLOP/s (140 us with no load after the first, 120 without the sums of x as well).
-template <int G>
-__global__ __launch_bounds__(256, 2) void gemm_w4_long_kernel(const bf16_t* __restrict__ x, const uint8_t* __restrict__ q,
-                                                              const uint32_t* __restrict__ sz, Out out, int M, int N, int K) {
-    using Cols = W4Cols<G, 2>;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds0[128 * 256];
-    __shared__ __attribute__((aligned(1024))) uint8_t lds1[128 * 256];
-    __shared__ float zs[2][4][Taken<G, 2>::NP][64];
+// share their issue: of 320 instructions for a piece of 64 x 64 128 put codes in place, 128 scale two
+// groups' sums, 32 sum x, beside 36 matrix operations.  Measured on MI355X: 2,961 x 4096 x 4096 in groups of
+// 64 148 us back to back, 0.67 PFLOP/s; 4,096 x 4096 x 11008 in groups of 128 450 us, 0.82 PFLOP/s.
+template <int G, int NB>
+__device__ __forceinline__ void long_tile(const bf16_t* __restrict__ x, const uint8_t* __restrict__ q,
+                                          const uint32_t* __restrict__ sz, const Out& out, int M, int N, int K, int m0,
+                                          int col0, uint8_t* lds0, uint8_t* lds1, float (*zs)[4][2][64]) {
+    using Cols = W4Cols<G, NB>;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int row_blocks = (M + 127) / 128, col_blocks = (N + 127) / 128;
-    const int lid = xcd_logical(blockIdx.x, gridDim.x);
-    // strips of four row blocks, a column block after another (a block of x has four times the bytes
-    // of a block of codes: so the tiles that run at once share most of either)
-    const int strip = lid / (4 * col_blocks), in = lid - strip * 4 * col_blocks, high = min(4, row_blocks - 4 * strip);
-    const int m0 = (4 * strip + in % high) * 128, n0 = (in / high) * 128 + (wave & 1) * 64;
+    const int n0 = col0 + (wave & 1) * 32 * NB;
     // two waves share 64 rows: either sums the x of the half that it calls its first
     const int half = 32 * (wave & 1), r0 = (wave >> 1) * 64 + half, r1 = (wave >> 1) * 64 + (half ^ 32);
     const int lane = threadIdx.x & 63, row[2] = {r0 + (lane & 31), r1 + (lane & 31)};
     const Cols cols(q, sz, n0, N, K);
     const CodeConst cc;
-    f32x16 acc[2][2];
+    f32x16 acc[2][NB];
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
     const int n = K / 128;
@@ -570,13 +563,13 @@ __global__ __launch_bounds__(256, 2) void gemm_w4_long_kernel(const bf16_t* __re
         cols.load(j * 128, c);
     };
     // the zero points of the piece before, its sums now there from both waves
-    Taken<G, 2> taken;
+    Taken<G, NB> taken;
     auto take = [&](int u) {
 #pragma unroll
         for (int i = 0; i < taken.NP; ++i) {
             const float other = zs[u][wave ^ 1][i][lane];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < NB; ++b) {
                 acc[0][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(taken.sum[i], taken.corr[i][b], acc[0][b], 0, 0, 0);
                 acc[1][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(other, taken.corr[i][b], acc[1][b], 0, 0, 0);
             }
@@ -594,7 +587,7 @@ __global__ __launch_bounds__(256, 2) void gemm_w4_long_kernel(const bf16_t* __re
             landed();
             if (j + u + 1 < n) issue(j + u + 1, u ? lds0 : lds1, p[1 - u]);
             if (j + u > 0) take(1 - u);
-            mul_piece<G, 2>(u ? lds1 : lds0, row, p[u], cc, acc, taken);
+            mul_piece<G, NB>(u ? lds1 : lds0, row, p[u], cc, acc, taken);
 #pragma unroll
             for (int i = 0; i < taken.NP; ++i) zs[u][wave][i][lane] = taken.sum[i];
         }
@@ -606,12 +599,32 @@ __global__ __launch_bounds__(256, 2) void gemm_w4_long_kernel(const bf16_t* __re
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int m = m0 + (a ? r1 : r0) + row32(i), c = n0 + 32 * b + (threadIdx.x & 31);
                 if (m < M && c < N) out.put(m, c, N, acc[a][b][i]);
             }
+}
+
+constexpr int kLongSlots = 512;   // workgroups of the long kernel that run at once
+
+template <int G>
+__global__ __launch_bounds__(256, 2) void gemm_w4_long_kernel(const bf16_t* __restrict__ x, const uint8_t* __restrict__ q,
+                                                              const uint32_t* __restrict__ sz, Out out, int M, int N, int K,
+                                                              int whole) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds0[128 * 256];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds1[128 * 256];
+    __shared__ float zs[2][4][2][64];
+    const int row_blocks = (M + 127) / 128, col_blocks = (N + 127) / 128, b = blockIdx.x;
+    const int part = b < whole ? 0 : xcd_logical(b - whole, gridDim.x - whole);
+    const int lid = b < whole ? xcd_logical(b, whole) : whole + part / 2;
+    // strips of four row blocks, a column block after another (a block of x has four times the bytes
+    // of a block of codes: so the tiles that run at once share most of either)
+    const int strip = lid / (4 * col_blocks), in = lid - strip * 4 * col_blocks, high = min(4, row_blocks - 4 * strip);
+    const int m0 = (4 * strip + in % high) * 128, n0 = (in / high) * 128;
+    if (b < whole) long_tile<G, 2>(x, q, sz, out, M, N, K, m0, n0, lds0, lds1, zs);
+    else if (n0 + 64 * (part & 1) < N) long_tile<G, 1>(x, q, sz, out, M, N, K, m0, n0 + 64 * (part & 1), lds0, lds1, zs);
 }
 
 }  // namespace
@@ -659,10 +672,21 @@ hipError_t launch_gemm_w4(const void* x, const void* q, const void* sz, int32_t 
         return hipGetLastError();
     };
     const int64_t tiles = cdiv(M, 128) * cdiv(N, 128);
-    if (M > 64 && tiles >= 128)
-        return group == 128  ? go(gemm_w4_long_kernel<128>, tiles, 1, 256)
-               : group == 64 ? go(gemm_w4_long_kernel<64>, tiles, 1, 256)
-                             : go(gemm_w4_long_kernel<32>, tiles, 1, 256);
+    if (M > 64 && tiles >= 128) {
+        // Whole tiles in rounds, and a last round that would leave most places empty as halves of 64 columns,
+        // 4096 x 4096 in groups of 128: 128 tiles 35 us for 57, 256 54 (59), 384 81 (85), 448 97 (86); behind a
+        // whole round 640 117 us for 131, 736 135 (135), and in groups of 64 768 171 (168).  Below 128 tiles the
+        // decode tiles are as fast (96: 33 us, 35 in halves).
+        const int64_t rest = tiles % kLongSlots, most = tiles < kLongSlots ? kLongSlots * 3 / 4 : kLongSlots * 3 / 8;
+        const int64_t whole = rest <= most ? tiles - rest : tiles;
+        const int64_t grid = whole + 2 * (tiles - whole);
+        if (grid > INT32_MAX) return hipErrorInvalidValue;
+        auto run = [&](auto kern) {
+            hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), 0, s, xb, qb, zb, out, (int)M, (int)N, (int)K, (int)whole);
+            return hipGetLastError();
+        };
+        return group == 128 ? run(gemm_w4_long_kernel<128>) : group == 64 ? run(gemm_w4_long_kernel<64>) : run(gemm_w4_long_kernel<32>);
+    }
     const DecodeKind kind = decode_kind(M, N);
     return with_kind(group, kind, [&](auto g, auto k) {
         return go(gemm_w4_decode_kernel<g.value, k.value>, cdiv(N, tile_columns(kind)), cdiv(M, 64), kTileThreads);

@@ -84,3 +84,22 @@ def test_captured_calls(n_dec):
         torch.cuda.synchronize()
         assert np.array_equal(bits(own), bits(got_base))
         assert np.array_equal(bits(own)[row_ad < 0], bits(got)[row_ad < 0])
+
+
+@pytest.mark.parametrize("M,N,K,group", [(1100, 5636, 256, 64), (1100, 5636, 128, 128), (1290, 6660, 256, 32), (1300, 6700, 384, 128),
+                                         (2050, 7684, 128, 64)])
+def test_rounds_of_long_tiles(M, N, K, group):
+    """Tiles of 128 x 128 alone (405 of them), and whole ones with a last round of halves (583, 1,037)."""
+    say("long tiles", M, N, K, group)
+    import heterogeneous_adapter_gemm_amd as hg
+    g = np.random.default_rng(M + K)
+    scale, zero, w, packed, sz = weight(g, N, K, group)
+    x = bf16(g, M, K)
+    y = torch.full((M + 1, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    hg.base_gemm_w4(dev(x), packed, sz, y, M, N, K, group)
+    y2 = torch.empty_like(y)
+    hg.base_gemm_w4(dev(x), packed, sz, y2, M, N, K, group)
+    torch.cuda.synchronize()
+    assert np.array_equal(bits(y)[:M], bits(y2)[:M]) and np.all(to_np(y)[M] == 7.0)
+    want = x @ w.T
+    assert np.all(np.abs(to_np(y)[:M] - want) <= product_tolerance(want, x, scale, zero, K))
