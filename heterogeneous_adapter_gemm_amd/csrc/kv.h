@@ -35,13 +35,17 @@ struct KvAppendArgs {
 
 constexpr int kKvAppendBlocks = 1280;    // append workgroups that run at once
 constexpr int kKvRowTile = 16;           // query rows of a decode segment
+// Most query rows of a KV head that go in decode segments, up to four of them: 64 requests of about 2,100
+// tokens (32 heads over 8 of 128) 76 us for 109 with 8 rows each, 105 (130) with 12, 148 (146) with 16;
+// eight of about 1,750 22 (33), 27 (37), 29 (37); 33 x 36 rows of one head of 64 21 (26).
+constexpr int kKvFewRows = 64;
 constexpr int kKvPrefillRows = 128;      // query rows of a prefill segment
 // Waves that share the attention's work, as many as run at once by their registers: on each of
 // 256 CUs 16 (head_dim 64), 12 (128) or 8 (256).  A prefill worker is a workgroup of four, two a CU.
 constexpr int kKvPrefillWorkers = 512;
 constexpr int kv_workers(int head_dim) { return 1024 * (head_dim == 64 ? 4 : head_dim == 128 ? 3 : 2); }
-// An entry a worker, and two partial results of a row tile of fp32 sums and (m, l) each; where
-// sequences of few and of many rows may meet in a batch, both kinds' side by side.
+// An entry a worker, and two partial results of a row tile of fp32 sums and (m, l) each; from 17 query
+// rows on for both kinds of worker, side by side (sequences of few and of many rows may meet in a batch).
 constexpr int64_t kv_few_bytes(int head_dim) {
     return (int64_t)kv_workers(head_dim) * (36 + 2 * kKvRowTile * (head_dim + 2) * 4);
 }

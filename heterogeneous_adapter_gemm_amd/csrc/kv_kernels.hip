@@ -270,7 +270,7 @@ __global__ __launch_bounds__(256, D == 128 ? 5 : 4) void kv_append_kernel(KvArgs
 // that a border cuts leaves partial results, which a second launch joins.  Every workgroup
 // finds its piece from the device's lengths, so the launch does not depend on them (a captured
 // call follows them).
-enum KvClass { kKvAll = 0, kKvFew = 1, kKvMany = 2 };   // sequences: all, of at most kKvRowTile query rows, of more
+enum KvClass { kKvAll = 0, kKvFew = 1, kKvMany = 2 };   // sequences: all, of at most kKvFewRows query rows, of more
 
 struct KvCut {
     int rb_shift, cls, workers;
@@ -282,7 +282,7 @@ __device__ __forceinline__ int kv_steps(int tokens) { return (tokens + 31) >> 5;
 // have to be written too)
 __device__ __forceinline__ int kv_pairs(const KvArgs& b, const KvCut& cut, const KvSeq& q) {
     const int64_t rows = (int64_t)q.rows * b.group;
-    if ((cut.cls == kKvFew && rows > kKvRowTile) || (cut.cls == kKvMany && rows <= kKvRowTile)) return 0;
+    if ((cut.cls == kKvFew && rows > kKvFewRows) || (cut.cls == kKvMany && rows <= kKvFewRows)) return 0;
     return (int)((rows + (1 << cut.rb_shift) - 1) >> cut.rb_shift) * b.kv_heads;
 }
 __device__ __forceinline__ int kv_seg_steps(const KvSeq& q) { return max(1, kv_steps(q.len)); }
@@ -1645,7 +1645,7 @@ hipError_t attention(const KvArgs& b, const bf16_t* q, int64_t q_stride, bf16_t*
     if (most <= 2) return go(1, kv_decode_kernel<D, 4, true>);
     if (most <= 4) return go(2, kv_decode_kernel<D, 4, false>);
     if (most <= 8) return go(3, kv_decode_kernel<D, 2, false>);
-    if (most <= 16) return go(4, kv_decode_kernel<D, 1, false>);
+    if (most <= kKvFewRows) return go(4, kv_decode_kernel<D, 1, false>);
     KvBoth k;
     k.few = KvOut{out, out_stride, static_cast<uint8_t*>(workspace), share(4, kv_workers(D), 4)};
     k.many = KvOut{out, out_stride, k.few.ws + kv_few_bytes(D), share(7, kKvPrefillWorkers, 4)};
