@@ -37,7 +37,7 @@ constexpr int kKvAppendBlocks = 1280;    // append workgroups that run at once
 constexpr int kKvRowTile = 16;           // query rows of a decode segment
 // Most query rows of a KV head that go in decode segments, up to four of them: 64 requests of about 2,100
 // tokens (32 heads over 8 of 128) 76 us for 109 with 8 rows each, 105 (130) with 12, 148 (146) with 16;
-// eight of about 1,750 22 (33), 27 (37), 29 (37); 33 x 36 rows of one head of 64 21 (26).
+// eight of about 1,750 22 (33), 27 (37), 29 (37); 33 x 36 rows of one head of 64 19 (26).
 constexpr int kKvFewRows = 64;
 constexpr int kKvPrefillRows = 128;      // query rows of a prefill segment
 // Waves that share the attention's work, as many as run at once by their registers: on each of

@@ -1581,7 +1581,7 @@ __device__ __forceinline__ void merge_tile(const KvArgs& b, const KvOut& w, floa
 // ---------------------------------------------------------------- attention: kernels
 
 template <int D, int SUB, bool SPLIT>
-__global__ __launch_bounds__(256, D == 256 ? 2 : 3) void kv_decode_kernel(KvArgs b, const bf16_t* q, int64_t q_stride,
+__global__ __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) void kv_decode_kernel(KvArgs b, const bf16_t* q, int64_t q_stride,
                                                                           KvOut w, float c, KvCut cut) {
     decode_piece<D, SUB, SPLIT>(b, q, q_stride, w, c, cut, blockIdx.x);
 }
