@@ -204,70 +204,33 @@ __device__ __forceinline__ void rows_tile(const bf16_t* __restrict__ x, const ui
 
 // ---------------------------------------------------------------- 32-row operations
 
-// Codes and scales of a piece of 32 NB columns, in LDS: 2 KB of codes a block of 32 columns, a
-// lane's own 16 bytes (two of them) in a row, then the scales and zeros of a group, a word a lane.
+// Codes and scales of a piece of 32 NB columns, a lane's own.
 template <int G, int NB>
 struct W4Cols {
     static constexpr int NG = 128 / G, S = G / 16;   // groups of a piece; steps (words a lane) of a group
-    static constexpr int kBytes = NB * 2048 + NG * 256;
     struct Codes {
         uint32_t c[NB][NG][S], s[NB][NG];
     };
     const uint8_t* qn[NB];
-    const uint32_t *sn, *sb[NB];   // scales: a lane's of all the blocks' columns; of its column of each block
+    const uint32_t* sn[NB];
 
     __device__ __forceinline__ W4Cols(const uint8_t* q, const uint32_t* sz, int n0, int N, int K) {
         const int lane = threadIdx.x & 63, lr = lane & 31, hg = lane >> 5;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-        {
+        for (int b = 0; b < NB; ++b) {
             const int64_t n = min(n0 + 32 * b + lr, N - 1);
-            qn[b] = q + n * (K / 2) + hg * (G == 128 ? 32 : 16);
-            sb[b] = sz + n * (K / G);
+            qn[b] = q + n * (K / 2) + hg * (G / 4);
+            sn[b] = sz + n * (K / G);
         }
-        sn = sz + (int64_t)min(n0 + (NB == 2 ? lane : lr), N - 1) * (K / G);
     }
-    // straight to registers
     __device__ __forceinline__ void load(int kb, Codes& p) const {
-        const int hg = (threadIdx.x & 63) >> 5;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                ld_words(qn[b] - hg * (G == 128 ? 32 : 16) + (kb + g * G) / 2 + hg * (G / 4), p.c[b][g]);
-                p.s[b][g] = sb[b][kb / G + g];
+                ld_words(qn[b] + (kb + g * G) / 2, p.c[b][g]);
+                p.s[b][g] = sn[b][kb / G + g];
             }
-    }
-    __device__ __forceinline__ void load(int kb, uint8_t* to) const {
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                global_load_lds16(qn[b] + kb / 2 + i * (G == 128 ? 16 : 32), to + (2 * b + i) * 1024);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) global_load_lds4(sn + kb / G + g, to + NB * 2048 + g * 256);
-    }
-    __device__ __forceinline__ void read(const uint8_t* from, Codes& p) const {
-        const int lane = threadIdx.x & 63, lr = lane & 31, hg = lane >> 5;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if constexpr (G == 32) {
-                    // a lane's 16 bytes are one group of its column: it wants half of both
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        ld_words(from + (2 * b + i) * 1024 + (32 * u + lr) * 16 + hg * 8, p.c[b][2 * i + u]);
-                } else {
-                    const u32x4 v = ld16(from + (2 * b + i) * 1024 + lane * 16);
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) p.c[b][G == 128 ? 0 : i][G == 128 ? 4 * i + y : y] = v[y];
-                }
-            }
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-                p.s[b][g] = *reinterpret_cast<const uint32_t*>(from + NB * 2048 + g * 256 + (32 * b + lr) * 4);
-        }
     }
 };
 
