@@ -315,8 +315,8 @@ __device__ __forceinline__ int row32(int i) { return 8 * (i / 4) + 4 * ((threadI
 // flight) and no barrier until their sums meet there.  Two waves a SIMD, so that one's conversions run
 // beside the other's matrix operations.  Bound by the vector units (300 instructions for a piece of 64 x
 // 64 beside 36 matrix operations) and the latency of x from L2, half a step of it open.  Measured on
-// MI355X, 64 rows: 4096 -> 11008 17 us, 4096 -> 4096 12 us; of the 17, 2 until the first x is there, 2 for the
-// sums of the waves.  (Four waves with whole pieces took 20 us and 17.5; reading a word of each
+// MI355X, 64 rows: 4096 -> 11008 17 us, 4096 -> 4096 8.5 us; of the 17, 2 until the first x is there, 2 for the
+// sums of the waves.  (Four waves with whole pieces took 20 us; reading a word of each
 // column's codes four pieces ahead 20 us.)
 constexpr int kDecodeWaves = 8;
 
@@ -415,8 +415,9 @@ __device__ __forceinline__ void decode_tile(const bf16_t* __restrict__ x, const 
         }
     };
     const int n = (K / 128 - wave + W - 1) / W;   // pieces of this wave
-    // (each workgroup begins at a piece of its own, so that they do not all read one slice of x at once)
-    const int shift = n > 0 ? bx % n : 0;
+    // (each 64 columns begin at a piece of their own, so that not all workgroups read one slice of x at
+    // once; by the columns, so that every kind of tile has the same sums)
+    const int shift = n > 0 ? (n0 >> 6) % n : 0;
     auto at = [&](int j) { return (wave + W * (j + shift < n ? j + shift : j + shift - n)) * 128; };
     Codes p[2];
     if (n > 0) issue(at(0), 0, p[0]);
@@ -466,6 +467,7 @@ __device__ __forceinline__ void any_tile(const bf16_t* __restrict__ x, const uin
 }
 constexpr int kTileThreads = 64 * kDecodeWaves;
 static_assert(kRowWaves == kDecodeWaves, "one workgroup size for every kind");
+constexpr int tile_rows(int kind) { return kind == kRows16 ? 16 : kind == kRows32 ? 32 : 64; }
 constexpr int tile_columns(int kind) { return kind == kRows16 ? 16 : kind == kRows64Wide ? 64 : 32; }
 
 template <int G, int KIND>
@@ -478,15 +480,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void gemm_w4_decode_kernel(const b
 
 // Decode batches of up to 64 rows with adapters: the tiles, the BGMV shrink's units (two a
 // workgroup) and the copy of a plan's index in one launch.  Measured on MI355X, 64 rows 4096 -> 4096, the
-// whole call: 16 adapters of rank 16 15.4 us (21.5 with a launch of their own for the units), 64 of rank 64
-// 29.4 us (36.3).
+// whole call: 16 adapters of rank 16 15.4 us, 64 of rank 64 29.3 us (21.5 and 36.3 with a launch of their own
+// for the units).
 template <int G, int KIND>
 __global__ __launch_bounds__(kTileThreads, 2) void gemm_w4_shrink_kernel(
     const bf16_t* __restrict__ x, const uint8_t* __restrict__ q, const uint32_t* __restrict__ sz, Out out, int M, int N, int K,
-    LoraArgs a, int n_gemm, int n_unit, const uint32_t* __restrict__ cp_src, uint32_t* __restrict__ cp_dst, int cp_n) {
+    LoraArgs a, int n_gemm, int n_cols, int n_unit, const uint32_t* __restrict__ cp_src, uint32_t* __restrict__ cp_dst, int cp_n) {
     const int b = blockIdx.x;
     if (b < n_gemm) {
-        any_tile<G, KIND>(x, q, sz, out, M, N, K, b, 0);
+        any_tile<G, KIND>(x, q, sz, out, M, N, K, b % n_cols, b / n_cols);
     } else if (b < n_gemm + n_unit) {
         const int wave = threadIdx.x >> 6;
         bgmv_shrink_unit<bf16_t, true>(a, 2 * (b - n_gemm) + wave / 4, a.lp_per_rank, a.v, wave % 4);
@@ -598,13 +600,17 @@ bool gemm_w4_ok(int64_t M, int64_t N, int64_t K, int32_t group) {
     return M * K * 2 < INT32_MAX && N * K / 2 < INT32_MAX;
 }
 
-// Up to 64 rows, and blocks of 64 of more; 64 columns wide where that still makes 160 workgroups (each
-// reads all of x: 64 rows 4096 -> 11008 18 us so, 22 us with 32 columns; 4096 -> 4096 12 us with 32
-// columns, 18 us with 64).
-static DecodeKind decode_kind(int64_t M, int64_t N) {
-    return M <= 16 ? kRows16 : M <= 32 ? kRows32 : N >= 64 * 160 ? kRows64Wide : kRows64;
-}
 static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// Blocks of 32 rows where every tile then has a compute unit of its own (each reads all of its rows' x; 64
+// rows: 4096 -> 4096 8.5 us for 11.4 with blocks of 64, 11008 -> 4096 17 (24), but 4096 -> 6144 13.5 (11.6));
+// `others` workgroups beside them need one too (with 40 of BGMV units 4096 -> 4096 takes 14.5 us for 12).
+// Else blocks of 64, 64 columns wide where 32 would take a second round (64 rows 4096 -> 11008 17 us so, 22 with
+// 32 columns; 4096 -> 4096 12 with 32 columns, 18 with 64).
+static DecodeKind decode_kind(int64_t M, int64_t N, int64_t others) {
+    if (M <= 16) return kRows16;
+    if (M <= 32 || cdiv(M, 32) * cdiv(N, 32) + others <= 256) return kRows32;
+    return cdiv(M, 64) * cdiv(N, 32) > 256 ? kRows64Wide : kRows64;
+}
 
 // f(integral_constant group, integral_constant kind)
 template <typename F>
@@ -650,9 +656,9 @@ hipError_t launch_gemm_w4(const void* x, const void* q, const void* sz, int32_t 
         };
         return group == 128 ? run(gemm_w4_long_kernel<128>) : group == 64 ? run(gemm_w4_long_kernel<64>) : run(gemm_w4_long_kernel<32>);
     }
-    const DecodeKind kind = decode_kind(M, N);
+    const DecodeKind kind = decode_kind(M, N, 0);
     return with_kind(group, kind, [&](auto g, auto k) {
-        return go(gemm_w4_decode_kernel<g.value, k.value>, cdiv(N, tile_columns(kind)), cdiv(M, 64), kTileThreads);
+        return go(gemm_w4_decode_kernel<g.value, k.value>, cdiv(N, tile_columns(kind)), cdiv(M, tile_rows(kind)), kTileThreads);
     });
 }
 
@@ -665,12 +671,13 @@ hipError_t launch_gemm_w4_shrink(const void* x, const void* q, const void* sz, i
                                  const void* cp_src, void* cp_dst, int64_t cp_n, hipStream_t s) {
     if (!gemm_w4_shrink_fits(M, N, K, group, a.n_su) || cp_n < 0 || cp_n > INT32_MAX) return hipErrorInvalidValue;
     const Out out{static_cast<bf16_t*>(y), ybase, row_slot, raw_mask};
-    const DecodeKind kind = decode_kind(M, N);
-    const int tn = (int)cdiv(N, tile_columns(kind)), nu = (a.n_su + 1) / 2, ncp = cp_n > 0 ? kCopyBlocks : 0;
+    const int nu = (a.n_su + 1) / 2, ncp = cp_n > 0 ? kCopyBlocks : 0;
+    const DecodeKind kind = decode_kind(M, N, nu + ncp);
+    const int tn = (int)cdiv(N, tile_columns(kind)), tiles = tn * (int)cdiv(M, tile_rows(kind));
     return with_kind(group, kind, [&](auto g, auto k) {
-        hipLaunchKernelGGL((gemm_w4_shrink_kernel<g.value, k.value>), dim3((unsigned)(tn + nu + ncp)), dim3(kTileThreads), 0, s,
+        hipLaunchKernelGGL((gemm_w4_shrink_kernel<g.value, k.value>), dim3((unsigned)(tiles + nu + ncp)), dim3(kTileThreads), 0, s,
                            static_cast<const bf16_t*>(x), static_cast<const uint8_t*>(q), static_cast<const uint32_t*>(sz), out,
-                           (int)M, (int)N, (int)K, a, tn, nu, static_cast<const uint32_t*>(cp_src),
+                           (int)M, (int)N, (int)K, a, tiles, tn, nu, static_cast<const uint32_t*>(cp_src),
                            static_cast<uint32_t*>(cp_dst), (int)cp_n);
         return hipGetLastError();
     });

@@ -103,3 +103,22 @@ def test_rounds_of_long_tiles(M, N, K, group):
     assert np.array_equal(bits(y)[:M], bits(y2)[:M]) and np.all(to_np(y)[M] == 7.0)
     want = x @ w.T
     assert np.all(np.abs(to_np(y)[:M] - want) <= product_tolerance(want, x, scale, zero, K))
+
+
+@pytest.mark.parametrize("n_dec,d_out,n_ad", [(40, 1024, 3), (64, 4096, 16), (64, 7000, 40), (64, 8192, 3), (33, 8064, 8), (64, 10240, 64)])
+def test_rows_without_an_adapter_are_the_base_products(n_dec, d_out, n_ad):
+    """Bit for bit, whatever tiles either call takes."""
+    say("rows without an adapter", n_dec, d_out, n_ad)
+    import heterogeneous_adapter_gemm_amd as hg
+    d_in, group = 1280, 128
+    g = np.random.default_rng(n_dec + d_out)
+    pool, ad, row_ad, plan, (scale, zero, w, packed, sz) = setup(g, d_in, d_out, [32] * n_ad, n_dec, group)
+    none = [-1 if i % 3 == 0 else pool.slot_of(i % n_ad) for i in range(n_dec)]
+    plan = pool.plan(None, None, none)
+    xd = dev(bf16(g, n_dec, d_in))
+    y, base = (torch.zeros((n_dec, d_out), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pool.linear_w4(plan, 0, 0, xd, packed, sz, group, y)
+    hg.base_gemm_w4(xd, packed, sz, base, n_dec, d_out, d_in, group)
+    torch.cuda.synchronize()
+    assert np.array_equal(bits(y)[::3], bits(base)[::3])
+    assert not np.array_equal(bits(y)[1::3], bits(base)[1::3])
