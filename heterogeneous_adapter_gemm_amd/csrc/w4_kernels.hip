@@ -501,7 +501,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void gemm_w4_shrink_kernel(
 // once for the four waves, one piece ahead.  Bound by the vector units and the matrix cores, which
 // share their issue: of 320 instructions for a piece of 64 x 64 128 put codes in place, 128 scale two
 // groups' sums, 32 sum x, beside 36 matrix operations.  Measured on MI355X: 2,961 x 4096 x 4096 in groups of
-// 64 148 us back to back, 0.67 PFLOP/s; 4,096 x 4096 x 11008 in groups of 128 450 us, 0.82 PFLOP/s.
+// 64 143 us back to back, 0.69 PFLOP/s; 4,096 x 4096 x 11008 in groups of 128 450 us, 0.82 PFLOP/s.
 template <int G, int NB>
 __device__ __forceinline__ void long_tile(const bf16_t* __restrict__ x, const uint8_t* __restrict__ q,
                                           const uint32_t* __restrict__ sz, const Out& out, int M, int N, int K, int m0,
@@ -641,11 +641,13 @@ hipError_t launch_gemm_w4(const void* x, const void* q, const void* sz, int32_t 
         return hipGetLastError();
     };
     const int64_t tiles = cdiv(M, 128) * cdiv(N, 128);
-    if (M > 64 && tiles >= 128) {
+    // From about four rounds of the decode tiles on the long ones (4096 inputs in groups of 128: 512 x 4096 31 us
+    // in decode tiles, 35 in long ones, 768 x 4096 45 (50), 300 x 11008 64 (79), 384 x 11008 75 (78), 1,024 x 4096 59
+    // (54), 520 x 11008 100 (86)).
+    if (M > 64 && cdiv(M, 64) * cdiv(N, 64) >= 1024) {
         // Whole tiles in rounds, and a last round that would leave most places empty as halves of 64 columns,
-        // 4096 x 4096 in groups of 128: 128 tiles 35 us for 57, 256 54 (59), 384 81 (85), 448 97 (86); behind a
-        // whole round 640 117 us for 131, 736 135 (135), and in groups of 64 768 171 (168).  Below 128 tiles the
-        // decode tiles are as fast (96: 33 us, 35 in halves).
+        // 4096 x 4096 in groups of 128: 256 tiles 54 us for 59, 384 81 (85), 448 97 (86); behind a whole round
+        // 640 117 us for 131, 736 135 (135), and in groups of 64 768 171 (168).
         const int64_t rest = tiles % kLongSlots, most = tiles < kLongSlots ? kLongSlots * 3 / 4 : kLongSlots * 3 / 8;
         const int64_t whole = rest <= most ? tiles - rest : tiles;
         const int64_t grid = whole + 2 * (tiles - whole);

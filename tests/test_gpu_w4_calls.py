@@ -87,9 +87,10 @@ def test_captured_calls(n_dec):
 
 
 @pytest.mark.parametrize("M,N,K,group", [(1100, 5636, 256, 64), (1100, 5636, 128, 128), (1290, 6660, 256, 32), (1300, 6700, 384, 128),
-                                         (2050, 7684, 128, 64)])
+                                         (2050, 7684, 128, 64), (1030, 4200, 256, 64), (1030, 4200, 128, 32), (1090, 4100, 384, 128)])
 def test_rounds_of_long_tiles(M, N, K, group):
-    """Tiles of 128 x 128 alone (405 of them), and whole ones with a last round of halves (583, 1,037)."""
+    """Tiles of 128 x 128 alone (405 of them), whole ones with a last round of halves (583, 1,037), halves
+    alone (297)."""
     say("long tiles", M, N, K, group)
     import heterogeneous_adapter_gemm_amd as hg
     g = np.random.default_rng(M + K)
