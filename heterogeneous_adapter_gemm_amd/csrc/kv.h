@@ -33,7 +33,8 @@ struct KvAppendArgs {
     int32_t rot, interleaved;
 };
 
-constexpr int kKvAppendBlocks = 1280;    // append workgroups that run at once
+// Append workgroups that run at once, by their registers: five on each of 256 CUs (head_dim 128) or four
+constexpr int64_t kv_append_blocks(int head_dim) { return 256 * (head_dim == 128 ? 5 : 4); }
 constexpr int kKvRowTile = 16;           // query rows of a decode segment
 // Most query rows of a KV head that go in decode segments, up to four of them: 64 requests of about 2,100
 // tokens (32 heads over 8 of 128) 76 us for 109 with 8 rows each, 105 (130) with 12, 148 (146) with 16;

@@ -75,18 +75,19 @@ constexpr int kSeqCache = 1024;   // row_start entries an append workgroup keeps
 
 // One row of one head per D / 8 lanes, 8 values a lane, and a workgroup for 16 consecutive rows
 // of a head (two heads or half the rows, by head_dim): a slab's bytes then come from one
-// workgroup, and meet in one L2 (one row of 16 heads a workgroup took 52 us for 2,769 rows of 32 +
+// workgroup, and meet in one L2 (one row of 16 heads a workgroup took 52 us for 2,286 rows of 32 +
 // 2 x 32 heads of 128).  Query rows are turned in fp32 and rounded once.  Key rows are turned in fp64
 // and rounded to bf16 (the key that an unquantised cache would hold) before they are
 // quantised: a code then depends on the exact product only, not on how it was summed, and
 // the quantisation itself works on bf16 values, whose halves, differences and quotients by
 // a bf16 step are the same in any order of evaluation.
-// Measured on MI355X: those 2,769 rows 44 us, 2.8 TB/s of rows and pages, about 300 vector instructions
-// for 512 values of a key or value (30 us of them; without its stores, or with fp32 for fp64, 42 us); 64
+// Measured on MI355X: those 2,286 rows 39 us, 3.2 TB/s of rows and pages, about 300 vector instructions
+// for 512 values of a key or value (30 us of them; its stores, or fp64, cost 2 us); 64
 // decode rows of 32 + 2 x 8 heads 5 us, launch and three dependent reads.
-// per_block: head groups a workgroup takes one after another, the next two's loads in flight.
+// blocks: workgroups that share 16 rows' head groups, each with every blocks-th (so that all have their
+// share of the keys, which cost most) one after another, the next two's loads in flight.
 template <int D>
-__global__ __launch_bounds__(256, D == 128 ? 5 : 4) void kv_append_kernel(KvArgs b, KvAppendArgs a, int per_block) {
+__global__ __launch_bounds__(256, D == 128 ? 5 : 4) void kv_append_kernel(KvArgs b, KvAppendArgs a, int blocks) {
     constexpr int LPR = D / 8, RPB = kv_append_rows(D), HPB = 256 / LPR / RPB;
     __shared__ int rs[kSeqCache];
     const int n_cache = min(b.n_seqs + 1, kSeqCache);
@@ -95,9 +96,9 @@ __global__ __launch_bounds__(256, D == 128 ? 5 : 4) void kv_append_kernel(KvArgs
     const int nq = a.q ? b.heads : 0;
     const int per_row = nq + 2 * b.kv_heads;
     const int c = threadIdx.x % LPR, g = threadIdx.x / LPR;
-    const int groups = (per_row + HPB - 1) / HPB, blocks = (groups + per_block - 1) / per_block;
+    const int groups = (per_row + HPB - 1) / HPB;
     const int t = (int)(blockIdx.x / blocks) * RPB + g % RPB;
-    const int first = (int)(blockIdx.x % blocks) * per_block, last = min(groups, first + per_block);
+    const int first = (int)(blockIdx.x % blocks);
     if (t >= b.n_rows) return;
     // the last sequence that starts at or before row t
     int lo = 0, hi = b.n_seqs;
@@ -250,12 +251,12 @@ __global__ __launch_bounds__(256, D == 128 ? 5 : 4) void kv_append_kernel(KvArgs
     };
     Item it[3];
     fetch(first, it[0]);
-    if (first + 1 < last) fetch(first + 1, it[1]);
-    for (int i = first; i < last; i += 3) {
+    if (first + blocks < groups) fetch(first + blocks, it[1]);
+    for (int i = first; i < groups; i += 3 * blocks) {
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
-            if (i + j >= last) break;
-            if (i + j + 2 < last) fetch(i + j + 2, it[(j + 2) % 3]);
+            if (i + j * blocks >= groups) break;
+            if (i + (j + 2) * blocks < groups) fetch(i + (j + 2) * blocks, it[(j + 2) % 3]);
             work(it[j]);
         }
     }
@@ -932,7 +933,7 @@ __device__ __forceinline__ bf16_t* out_row(const KvArgs& b, const KvOut& w, int 
 // Few query rows.  Workers are waves, each with all of its piece's segments by itself; where a
 // whole workgroup's piece is inside one segment its waves' sums meet in LDS, so that long
 // sequences leave a part a workgroup.  Bound by reading the cache once, and by the latency of a wave's
-// two steps in flight: measured on MI355X, 64 requests of about 2,250 tokens (32 heads over 8 of 128) 40 us,
+// two steps in flight: measured on MI355X, 64 requests of about 2,050 tokens (32 heads over 8 of 128) 40 us,
 // 3.6 TB/s of pages; 192 of 129 to 552 tokens, 32 KV heads with a query head each, 68 us, 4.1 TB/s; one of
 // 131,071 tokens 36 us, 4 TB/s; a lone one of 1,000 tokens 7.5 us, of which 3 us are finding its piece.
 template <int D, int SUB, bool SPLIT>
@@ -1662,14 +1663,15 @@ hipError_t attention(const KvArgs& b, const bf16_t* q, int64_t q_stride, bf16_t*
 hipError_t launch_kv_append(int head_dim, const KvArgs& b, const KvAppendArgs& a, hipStream_t s) {
     const int64_t per_row = (a.q ? b.heads : 0) + 2 * (int64_t)b.kv_heads;
     auto go = [&](auto kern, int lanes) {
-        // groups of heads a workgroup: one where they are few (latency), more where that still
-        // leaves about as many workgroups as run at once (2,769 rows of 96 heads of 128: 45 us, 53 with one group each)
+        // a workgroup for each group of heads where they are few (latency), no more than run at once where
+        // there are many (2,286 rows of 32 + 2 x 32 heads of 128 39 us; neighbouring heads a workgroup 45, all
+        // apart 53)
         const int rows = kv_append_rows(head_dim);
         const int64_t row_groups = (b.n_rows + rows - 1) / rows, groups = (per_row + lanes / rows - 1) / (lanes / rows);
-        const int per_block = (int)std::max<int64_t>(1, std::min(groups, (row_groups * groups + kKvAppendBlocks - 1) / kKvAppendBlocks));
-        const int64_t grid = row_groups * ((groups + per_block - 1) / per_block);
+        const int64_t blocks = std::max<int64_t>(1, std::min(groups, kv_append_blocks(head_dim) / row_groups));
+        const int64_t grid = row_groups * blocks;
         if (grid > INT32_MAX) return hipErrorInvalidValue;
-        hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), 0, s, b, a, per_block);
+        hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), 0, s, b, a, (int)blocks);
         return hipGetLastError();
     };
     switch (head_dim) {
