@@ -1195,9 +1195,12 @@ struct KvRows {
         for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
         if (__ballot(top > thr)) {
             float d = max_hg(top);
+            const bool fresh = thr < 0.f;
             if (!(d > thr)) d = 0.f;   // (not this row, or it has no token yet)
             else thr = 8.f;
-            const float al = __builtin_amdgcn_exp2f(-d);
+            // a row's first tokens set the scale of sums that are still zero: 2^-d of scores below -128
+            // is infinite, and zero times that not a number
+            const float al = fresh ? 1.f : __builtin_amdgcn_exp2f(-d);
             m += d;
             l *= al;
             z *= al;
