@@ -208,8 +208,9 @@ __global__ __launch_bounds__(256, D == 128 ? 5 : 4) void kv_append_kernel(KvArgs
             code[i] = fminf(code[i], 15.f);
         }
         // q is off by a few 2^-24: where a value is that near a border between two codes, where a
-        // reciprocal or a range overflows or the step is 0 or NaN, by the quotient itself
-        if (__ballot(!(off < 0.4999f) || !(inv < 1e30f))) {
+        // reciprocal or the row's range overflows (q is infinite there, and `off` leaves out its NaN) or the
+        // step is 0 or NaN, by the quotient itself
+        if (__ballot(!(off < 0.4999f) || !(inv < 1e30f) || !(mx - mn < INFINITY))) {
             const float half_step = step * 0.5f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
