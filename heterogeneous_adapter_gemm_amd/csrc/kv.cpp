@@ -146,7 +146,7 @@ int lora_kv_attention(lora_pool* pool, const lora_kv_batch* batch, const void* q
     if (empty) return on_device(b);
     const int64_t qw = (int64_t)batch->n_heads * batch->head_dim;
     if ((rc = check_rows("q", q, q_stride, qw)) || (rc = check_rows("out", out, out_stride, qw))) return rc;
-    const int64_t need = kv_workspace_bytes(batch->head_dim, b.group, batch->max_rows);
+    const int64_t need = kv_launch_bytes(batch->head_dim, b.group, batch->max_rows);
     if (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < need)
         return set_error(LORA_EINVAL, "workspace: %lld bytes, 16-byte aligned", (long long)need);
     if ((rc = on_device(b))) return rc;

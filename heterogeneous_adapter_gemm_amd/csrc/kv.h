@@ -45,14 +45,26 @@ constexpr int kKvPrefillRows = 128;      // query rows of a prefill segment
 // 256 CUs 16 (head_dim 64), 12 (128) or 8 (256).  A prefill worker is a workgroup of four, two a CU.
 constexpr int kKvPrefillWorkers = 512;
 constexpr int kv_workers(int head_dim) { return 1024 * (head_dim == 64 ? 4 : head_dim == 128 ? 3 : 2); }
-// An entry a worker, and two partial results of a row tile of fp32 sums and (m, l) each; from 17 query
-// rows on for both kinds of worker, side by side (sequences of few and of many rows may meet in a batch).
+// A batch whose sequences may have more query rows of a KV head than that runs the kernels of many rows
+// beside those of few (sequences of either kind may meet in it); the one rule for the launch and for
+// the workspace that it takes.
+constexpr bool kv_many_rows(int group, int max_rows) { return (int64_t)max_rows * group > kKvFewRows; }
+// An entry a worker, and two partial results of a row tile of fp32 sums and (m, l) each; for a batch of
+// many rows both kinds of worker's, side by side.
 constexpr int64_t kv_few_bytes(int head_dim) {
     return (int64_t)kv_workers(head_dim) * (36 + 2 * kKvRowTile * (head_dim + 2) * 4);
 }
+constexpr int64_t kv_many_bytes(int head_dim) {
+    return (int64_t)kKvPrefillWorkers * (36 + 2 * kKvPrefillRows * (head_dim + 2) * 4);
+}
+// What a call takes
+constexpr int64_t kv_launch_bytes(int head_dim, int group, int max_rows) {
+    return kv_few_bytes(head_dim) + (kv_many_rows(group, max_rows) ? kv_many_bytes(head_dim) : 0);
+}
+// What a caller is told to bring: from 17 query rows of a KV head on with the part of many rows, so that
+// up to four times the rows find room in it
 constexpr int64_t kv_workspace_bytes(int head_dim, int group, int max_rows) {
-    const int64_t many = (int64_t)kKvPrefillWorkers * (36 + 2 * kKvPrefillRows * (head_dim + 2) * 4);
-    return kv_few_bytes(head_dim) + ((int64_t)max_rows * group <= kKvRowTile ? 0 : many);
+    return kv_few_bytes(head_dim) + ((int64_t)max_rows * group > kKvRowTile ? kv_many_bytes(head_dim) : 0);
 }
 
 hipError_t launch_kv_append(int head_dim, const KvArgs& b, const KvAppendArgs& a, hipStream_t s);

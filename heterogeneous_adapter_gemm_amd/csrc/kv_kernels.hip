@@ -1650,7 +1650,7 @@ hipError_t attention(const KvArgs& b, const bf16_t* q, int64_t q_stride, bf16_t*
     if (most <= 2) return go(1, kv_decode_kernel<D, 4, true>);
     if (most <= 4) return go(2, kv_decode_kernel<D, 4, false>);
     if (most <= 8) return go(3, kv_decode_kernel<D, 2, false>);
-    if (most <= kKvFewRows) return go(4, kv_decode_kernel<D, 1, false>);
+    if (!kv_many_rows(b.group, max_rows)) return go(4, kv_decode_kernel<D, 1, false>);
     KvBoth k;
     k.few = KvOut{out, out_stride, static_cast<uint8_t*>(workspace), share(4, kv_workers(D), 4)};
     k.many = KvOut{out, out_stride, k.few.ws + kv_few_bytes(D), share(7, kKvPrefillWorkers, 4)};

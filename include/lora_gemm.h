@@ -458,7 +458,9 @@ int lora_kv_pages_per_block(const lora_pool* pool, int32_t n_kv_heads, int32_t h
 
 /* Device workspace lora_kv_attention needs for a batch (from head_dim, the
  * head counts and max_rows only).  Nothing in it needs to start at zero.  Calls
- * that overlap need one each. */
+ * that overlap need one each.  Where a sequence may have more than 16 query rows
+ * of a KV head (max_rows * n_heads / n_kv_heads) the size has room for prompts;
+ * the call itself takes the smaller size up to 64 of them. */
 int lora_kv_workspace_bytes(const lora_kv_batch* batch, int64_t* out_bytes);
 
 /* Append: the rows' keys and values to their pages, and q to q_out, the first

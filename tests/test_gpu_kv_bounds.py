@@ -90,3 +90,28 @@ def test_large_values_keep_their_room(G, rows):
     q, k, v = ordinary(g, sum(rows), G, 1, 500, D)
     assert max(np.abs(x).max() for x in (q, k, v)) < 8
     check(D, G, 1, 1024, rows, lens, q * 2.0 ** 53, k * 2.0 ** 53, v * 2.0 ** 53, scale=2.0 ** -106 * D ** -0.5)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,n", [(5, 4), (4, 16), (64, 1)])
+def test_up_to_64_query_rows_in_the_workspace_of_few(D, G, n):
+    """The workspace of sequences of 16 query rows of a KV head, and nothing behind it touched."""
+    import heterogeneous_adapter_gemm_amd as hg
+    from tests.gpu_helpers import to_np
+    from tests.test_gpu_kv import dev
+    say("small workspace", D, G, n)
+    g = np.random.default_rng(D + G)
+    rows, lens = [n, 1, n], [900, 40, n]
+    pool = make_pool(2048, blocks(lens) * 2 + 3)
+    b, _ = make_batch(pool, G, 1, D, rows, lens)
+    q, k, v = ordinary(g, sum(rows), G, 1, sum(lens), D)
+    attend(pool, b, lens, q, k, v, D ** -0.5)
+    few = hg.lora_kv_workspace_bytes(hg.lora_kv_batch(1, 1, D, 1, 1, 1, 1, 0, None, None, None))
+    assert few < hg.lora_kv_workspace_bytes(b.c)
+    ws = torch.full((few + 4096,), 255, dtype=torch.uint8, device="cuda")
+    out = torch.empty(q.shape, dtype=torch.bfloat16, device="cuda")
+    pool.kv_attention(b, dev(q), out, workspace=ws[:few])
+    torch.cuda.synchronize()
+    assert bool((ws[few:] == 255).all())
+    want, bound, _ = batch_bounds(q, KV.quantise(k), KV.quantise(v), rows, lens, 1, D ** -0.5)
+    assert not outside(to_np(out), want, bound).any()
