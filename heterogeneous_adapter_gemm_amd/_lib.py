@@ -227,7 +227,7 @@ def _stream(stream) -> Optional[int]:
 
 
 def _on_gpu(stream, call, *tensors) -> None:
-    """call(stream) on the GPU that holds the tensors, whichever is current (addresses: on the current one)."""
+    """call(stream) on the GPU that holds the tensors, whichever is current (addresses alone: on the current one)."""
     dev = None
     for t in tensors:
         if isinstance(t, int) or t is None:
@@ -257,6 +257,7 @@ class Pool:
         self.desc = desc
         self._keep = keep
         self.engines: set = set()   # handles of live engines over this pool, destroyed first
+        self.pages = None           # the tensor of the pages, where there is one: the pool's GPU
 
     def __del__(self):
         if getattr(self, "handle", None) and _LIB is not None:
@@ -502,7 +503,7 @@ def lora_linear_w4(pool: Pool, plan: Plan, layer: int, proj: int, x, w0_code, w0
                    stream=None) -> None:
     _on_gpu(stream, lambda st: _check(library().lora_linear_w4(pool.handle, plan.handle, layer, proj, _addr(x),
                                                                _addr(w0_code), _addr(w0_scale), group, _addr(y), st),
-                                      "lora_linear_w4"), x, w0_code, w0_scale, y)
+                                      "lora_linear_w4"), pool.pages, x, w0_code, w0_scale, y)
 
 
 def lora_kv_pages_per_block(pool: Pool, n_kv_heads: int, head_dim: int) -> int:

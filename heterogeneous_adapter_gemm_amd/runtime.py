@@ -114,6 +114,7 @@ class DevicePool:
                 desc.stage_dev = self.stage.data_ptr()
                 desc.stage_bytes = stage_bytes
         self.pool = L.lora_pool_create(desc, keep)
+        self.pool.pages = self.pages
         self._host: Dict[int, tuple] = {}
         self._kv_pages: Dict[tuple, int] = {}
 
