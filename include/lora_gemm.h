@@ -376,7 +376,12 @@ int lora_linear_fp8(lora_pool* pool, const lora_plan* plan, int32_t layer, int32
  * the codes, which are exact in bf16; scale and zero are applied to fp32 sums
  * of a group), output rounded to bf16 once.
  * Requires N % 4 == 0, K % 128 == 0, 16-byte aligned pointers, M * K * 2 and
- * N * K / 2 below 2^31.  M = 0 is a no-op.  Errors: EINVAL, EHIP. */
+ * N * K / 2 below 2^31.  M = 0 is a no-op.
+ * The cores' sums run over 16 + code, and 16 + zero times the sum of x is taken
+ * away.  So a row of x that holds an infinity or NaN is NaN in every column (also
+ * where the product itself would be an infinity), and one for which (32 + |zero|)
+ * sum |x| over a group, or scale times that over the row, passes fp32's range may
+ * come out as infinity or NaN where y would fit.  Errors: EINVAL, EHIP. */
 int base_gemm_w4(const void* x, const void* w0_code, const void* w0_scale, void* y, int64_t M, int64_t N, int64_t K,
                  int32_t group, void* stream);
 
