@@ -73,19 +73,18 @@ constexpr int kv_append_rows(int head_dim) { return head_dim == 256 ? 8 : 16; }
 
 constexpr int kSeqCache = 1024;   // row_start entries an append workgroup keeps in LDS
 
-// One row of one head per D / 8 lanes, 8 values a lane, and a workgroup for 16 consecutive rows
-// of a head (two heads or half the rows, by head_dim): a slab's bytes then come from one
-// workgroup, and meet in one L2 (one row of 16 heads a workgroup took 52 us for 2,286 rows of 32 +
-// 2 x 32 heads of 128).  Query rows are turned in fp32 and rounded once.  Key rows are turned in fp64
-// and rounded to bf16 (the key that an unquantised cache would hold) before they are
-// quantised: a code then depends on the exact product only, not on how it was summed, and
+// One row of one head per D / 8 lanes, 8 values a lane.  A workgroup has 16 consecutive rows (8 of 256
+// values) and, one after another, every blocks-th group of their heads (a head, of 64 values two), `blocks`
+// workgroups sharing the rows, so that all have their share of the keys, which cost most; the next two
+// groups' loads are in flight.  A slab's bytes then come from one workgroup, and meet in one L2 (one row of
+// 16 heads a workgroup took 52 us for 2,286 rows of 32 + 2 x 32 heads of 128).  Query rows are turned in fp32.
+// Key rows are turned in fp64 and rounded to bf16 (the key that an unquantised cache would hold) before
+// they are quantised: a code then depends on the exact product only, not on how it was summed, and
 // the quantisation itself works on bf16 values, whose halves, differences and quotients by
 // a bf16 step are the same in any order of evaluation.
-// Measured on MI355X: those 2,286 rows 39 us, 3.2 TB/s of rows and pages, about 300 vector instructions
+// Measured on MI355X: those 2,286 rows 37 us, 3.4 TB/s of rows and pages, about 300 vector instructions
 // for 512 values of a key or value (30 us of them; its stores, or fp64, cost 2 us); 64
 // decode rows of 32 + 2 x 8 heads 5 us, launch and three dependent reads.
-// blocks: workgroups that share 16 rows' head groups, each with every blocks-th (so that all have their
-// share of the keys, which cost most) one after another, the next two's loads in flight.
 template <int D>
 __global__ __launch_bounds__(256, D == 128 ? 5 : 4) void kv_append_kernel(KvArgs b, KvAppendArgs a, int blocks) {
     constexpr int LPR = D / 8, RPB = kv_append_rows(D), HPB = 256 / LPR / RPB;
@@ -1080,8 +1079,10 @@ __device__ __forceinline__ void decode_piece(const KvArgs& b, const bf16_t* q, i
 //
 // 32-row matrix operations: lane (r, hg) = (lane % 32, lane / 32) holds everything of query row r:
 // of 32 tokens' scores those of tokens 8 x + 4 hg .. + 3 (x 0..3), of the output as store() says.
-// The weights are rounded to bf16 once here (half a step is 2^-9 of a weight on average, as much
-// as the output's own rounding; a second half would cost half as many matrix operations again).
+// The weights are rounded to bf16 once here, by at most 2^-8 of a weight, as much as the output's own
+// rounding and, unlike that one, with different signs from token to token (four pieces of 512 rows: 0.0024 of
+// the outputs' size from the exact ones, 0.0017 of it the output's rounding); a second half, as few rows
+// have it, would cost half as many matrix operations again.
 // z and the sum of the rounded weights put the codes' 16 and lo in: o = sum w' (16 + code) +
 // sum p (lo + 8 step) - 24 sum w', so that the rounding counts for code - 8 only.
 template <int D>

@@ -40,7 +40,9 @@ def device_tensor(arr: np.ndarray, device="cuda"):
 class KvBatch:
     """A batch over the pool's KV pages (lora_kv_batch in the C header): device int32 tensors
     row_start [n_seqs + 1], ctx_len [n_seqs] and page_table [n_seqs, max_blocks, pages per block]
-    (one layer's), n_rows rows of q, k and v, at most max_rows of one sequence (None: n_rows).
+    (one layer's), n_rows rows of q, k and v, at most max_rows of one sequence (None: n_rows, since the
+    lengths are on the device; decode batches give it: from more than 64 query rows of a KV head on
+    the kernels of prompts run beside those of few rows, and take their workspace).
     The tensors are read when the kernels run: a caller may write new lengths or pages into
     them between calls, and between replays of a captured one."""
 

@@ -471,7 +471,8 @@ int lora_kv_workspace_bytes(const lora_kv_batch* batch, int64_t* out_bytes);
 /* Append: the rows' keys and values to their pages, and q to q_out, the first
  * rot_dim values of every q and k head turned by their position's angles: pairs
  * (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved, (a, b) -> (a cos - b
- * sin, b cos + a sin).  cos_sin: device fp32 [rot_positions][rot_dim], rot_dim / 2
+ * sin, b cos + a sin), keys in fp64 and queries in fp32, then rounded to bf16.
+ * cos_sin: device fp32 [rot_positions][rot_dim], rot_dim / 2
  * cosines then as many sines; NULL with rot_dim 0: no rotation.  rot_dim a
  * multiple of 16 up to head_dim; rot_positions at least 16 max_blocks.  Bytes of a
  * block past its last token stay as they are.  Two rows of one batch must not
@@ -483,8 +484,14 @@ int lora_kv_append(lora_pool* pool, const lora_kv_batch* batch, const lora_kv_ro
  * tokens at positions up to the row's own of scale * q . key, times the values.
  * q (already turned) and out: bf16 [n_rows][n_heads][head_dim] with row strides as
  * in lora_kv_rows.  Scores, softmax sums and outputs are held in fp32; the output
- * is rounded once.  The same inputs give the same bits.  scale > 0 and finite.
- * Errors: EINVAL, EHIP. */
+ * is rounded once.  On their way into the matrix cores the softmax weights, times
+ * their value's step, are rounded to bf16: as two halves (2^-16 of a weight is
+ * lost) in sequences of up to 64 query rows of a KV head (rows * n_heads /
+ * n_kv_heads) and in batches whose max_rows says no more, as one (2^-8) in longer
+ * ones.  The sums run over 16 + code and are not normalised: q, keys and values
+ * of up to 2^56 in size have their room; beyond, a row may come out as infinity or
+ * NaN where the output would fit.  The same inputs give the same bits.  scale > 0
+ * and finite.  Errors: EINVAL, EHIP. */
 int lora_kv_attention(lora_pool* pool, const lora_kv_batch* batch, const void* q, int64_t q_stride, void* out,
                       int64_t out_stride, float scale, void* workspace, int64_t workspace_bytes, void* stream);
 
