@@ -566,7 +566,11 @@ typedef struct lora_engine_desc {
     int32_t prefetch_window;       /* waiting requests looked ahead at, >= 0 */
     int32_t admit_in_flight;       /* 0 or 1, see step 3 */
     int32_t max_wait_steps;        /* starvation bound in steps; 0 = none */
-    int32_t kv_pages_per_token;    /* >= 0; 0 = the caller manages KV pages */
+    int32_t kv_pages_per_token;    /* >= 0; 0 = the caller manages KV pages.  The lora_kv_* calls take
+                                      pages by blocks of 16 tokens: layers x lora_kv_pages_per_block
+                                      a token covers requests of any length, with 16 times the pages of
+                                      a long one; a caller who cannot spare them sets 0 and takes each
+                                      block's pages by lora_pool_alloc_kv */
     int32_t reserved;              /* 0 */
     lora_adapter_info_fn info;
     lora_adapter_fill_fn fill;
