@@ -313,11 +313,12 @@ __device__ __forceinline__ int row32(int i) { return 8 * (i / 4) + 4 * ((threadI
 // Decode batches: 32 MB rows by 32 NB columns a workgroup, its eight waves taking the 128-deep
 // pieces of K in turn, in halves, each with its own place for x in LDS (two halves, the next one in
 // flight) and no barrier until their sums meet there.  Two waves a SIMD, so that one's conversions run
-// beside the other's matrix operations.  Bound by the vector units (300 instructions for a piece of 64 x
-// 64 beside 36 matrix operations) and the latency of x from L2, half a step of it open.  Measured on
-// MI355X, 64 rows: 4096 -> 11008 17 us, 4096 -> 4096 8.5 us; of the 17, 2 until the first x is there, 2 for the
-// sums of the waves.  (Four waves with whole pieces took 20 us; reading a word of each
-// column's codes four pieces ahead 20 us.)
+// beside the other's matrix operations (300 vector instructions for a piece of 64 x 64, 36 matrix
+// operations).  Bound by the latency of x from L2, half a step of it open, and by the tiles' number where
+// they leave compute units without one: 4096 -> 11008 has 172 for 256, vector instructions issue in 38 % of a
+// SIMD's cycles and matrix operations in 17 %.  Measured on MI355X, 64 rows: 4096 -> 11008 16 us, 4096 -> 4096
+// 8.5 us; of the 16, 2 until the first x is there, 2 for the sums of the waves.  (Four waves with whole
+// pieces took 20 us; reading a word of each column's codes four pieces ahead 20 us.)
 constexpr int kDecodeWaves = 8;
 
 template <int G, int MB, int NB>
