@@ -1669,7 +1669,7 @@ hipError_t launch_kv_append(int head_dim, const KvArgs& b, const KvAppendArgs& a
     const int64_t per_row = (a.q ? b.heads : 0) + 2 * (int64_t)b.kv_heads;
     auto go = [&](auto kern, int lanes) {
         // a workgroup for each group of heads where they are few (latency), no more than run at once where
-        // there are many (2,286 rows of 32 + 2 x 32 heads of 128 39 us; neighbouring heads a workgroup 45, all
+        // there are many (2,286 rows of 32 + 2 x 32 heads of 128 37 us; neighbouring heads a workgroup 45, all
         // apart 53)
         const int rows = kv_append_rows(head_dim);
         const int64_t row_groups = (b.n_rows + rows - 1) / rows, groups = (per_row + lanes / rows - 1) / (lanes / rows);

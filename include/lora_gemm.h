@@ -388,8 +388,9 @@ int base_gemm_w4(const void* x, const void* w0_code, const void* w0_scale, void*
 /* lora_linear with a 4-bit base (bf16 pool): y = x W0^T + delta with W0 as in
  * base_gemm_w4 (w0_code [d_out][d_in / 2], w0_scale [d_out][d_in / group]
  * pairs); the delta is lora_linear's, and rows with an adapter are rounded
- * once.  Errors as lora_linear, and EINVAL when the pool is not bf16 or the
- * shapes break base_gemm_w4's requirements. */
+ * once.  A call to be captured is not its plan's first one (which brings the
+ * plan's index to the device).  Errors as lora_linear, and EINVAL when the pool
+ * is not bf16 or the shapes break base_gemm_w4's requirements. */
 int lora_linear_w4(lora_pool* pool, const lora_plan* plan, int32_t layer, int32_t proj, const void* x,
                    const void* w0_code, const void* w0_scale, int32_t group, void* y, void* stream);
 
