@@ -62,7 +62,8 @@ constexpr int64_t kv_launch_bytes(int head_dim, int group, int max_rows) {
     return kv_few_bytes(head_dim) + (kv_many_rows(group, max_rows) ? kv_many_bytes(head_dim) : 0);
 }
 // What a caller is told to bring: from 17 query rows of a KV head on with the part of many rows, so that
-// up to four times the rows find room in it
+// it is room enough for prompts too
+static_assert(kKvRowTile <= kKvFewRows, "never less than a call takes");
 constexpr int64_t kv_workspace_bytes(int head_dim, int group, int max_rows) {
     return kv_few_bytes(head_dim) + ((int64_t)max_rows * group > kKvRowTile ? kv_many_bytes(head_dim) : 0);
 }
