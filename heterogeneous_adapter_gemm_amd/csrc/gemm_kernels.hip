@@ -30,6 +30,7 @@
 #include "bgmv_device.h"
 
 #include "common.h"
+#include "expand_device.h"
 #include "internal.h"
 
 namespace hagemm {
@@ -125,7 +126,7 @@ __device__ __forceinline__ void gemm_lds_tile(
     constexpr int UNIT_M = C::UNIT_M, SUB_M = UNIT_M / BM, SUB_N = UNIT_N / BN, SUBS = SUB_M * SUB_N;
     constexpr bool PIPE = C::PIPE;
     static_assert(SUB_M * BM == UNIT_M && SUB_N * BN == UNIT_N, "pieces tile the unit");
-    constexpr int NT = WM * WN * 64, NW = WM * WN;
+    constexpr int NW = WM * WN;
     constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
     constexpr int RB = BK * 2;          // bytes per tile row
     constexpr int CPR = RB / 16;        // 16-byte chunks per row
@@ -350,93 +351,11 @@ __device__ __forceinline__ void gemm_lds_tile(
     wait_vmcnt<0>();
 
     if constexpr (FUSE) {
-        // LDS after the K loop, per 32-wide slice of the rank: bt[n][j] = B[j0+j][n0+n],
-        // vh/vl[m][j] = high/low bf16 halves of gamma * v[m0+m][j0+j] for rows of the segment
-        // (zero elsewhere and past the rank).  Rows of 40 bf16 (80 B): fragment reads are
-        // free of bank conflicts.
-        constexpr int LDJ = 40;
-        static_assert(BN * LDJ * 2 <= STAGE && (S > 2 ? 1 : 2) * BM * LDJ * 2 <= STAGE, "fused epilogue LDS");
-        uint16_t* bt = reinterpret_cast<uint16_t*>(lds0);
+        // LDS after the K loop holds the expand's operands
+        static_assert(BN * kExpandRow * 2 <= STAGE && (S > 2 ? 1 : 2) * BM * kExpandRow * 2 <= STAGE, "fused epilogue LDS");
         uint16_t* vh = reinterpret_cast<uint16_t*>(lds1);
-        uint16_t* vl = S > 2 ? reinterpret_cast<uint16_t*>(lds2) : vh + BM * LDJ;
-        const int pmask = (1 << seg.page_shift) - 1;
-        for (int s = 0; s < seg.n_segs; ++s) {
-            const int sb = seg.s_begin[s], se = seg.s_end[s];
-            if (se <= m0 || sb >= m0 + BM) continue;
-            const int slot = seg.s_slot[s], r = seg.s_rank[s];
-            const float gamma = seg.s_gamma[s];
-            const int32_t* tabB =
-                seg.page_tab + (int64_t)slot * seg.slot_cap + (int64_t)r * seg.lp_per_rank + r * seg.nci;
-            for (int jb = 0; jb < r; jb += 32) {
-                __syncthreads();  // LDS free: the K loop, or the previous slice, is done with it
-                // item = (pair of rank-rows jp, 8 columns nv): the two rows' values of a column
-                // go to LDS as one 32-bit word; the lanes of a wave run along the pairs, so the
-                // stores of one instruction fall in distinct banks (at most two-way)
-                static_assert(LDJ % 2 == 0, "word-aligned rows");
-                uint32_t* btw = reinterpret_cast<uint32_t*>(bt);
-                for (int idx = threadIdx.x; idx < 16 * (BN / 8); idx += NT) {
-                    const int jp = idx & 15, nv = idx >> 4;
-                    const int n = min(n0 + nv * 8, N - 8);
-                    const int pg = n >> seg.page_shift, po = n & pmask;
-                    const int j0 = jb + 2 * jp;
-                    const bf16_t* pages = static_cast<const bf16_t*>(seg.pages);
-                    u32x4 v0 = ld16(pages + ((int64_t)tabB[min(j0, r - 1) * seg.nco + pg] << seg.page_shift) + po);
-                    u32x4 v1 = ld16(pages + ((int64_t)tabB[min(j0 + 1, r - 1) * seg.nco + pg] << seg.page_shift) + po);
-                    const bool nin = n0 + nv * 8 < N;
-                    if (j0 >= r || !nin) v0 = u32x4{0u, 0u, 0u, 0u};
-                    if (j0 + 1 >= r || !nin) v1 = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        btw[(nv * 8 + 2 * e) * (LDJ / 2) + jp] = (v0[e] & 0xFFFFu) | (v1[e] << 16);
-                        btw[(nv * 8 + 2 * e + 1) * (LDJ / 2) + jp] = (v0[e] >> 16) | (v1[e] & 0xFFFF0000u);
-                    }
-                }
-                for (int idx = threadIdx.x; idx < BM * 4; idx += NT) {
-                    const int ml = idx >> 2, j = (idx & 3) * 8;
-                    const int m = m0 + ml;
-                    float vv[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) vv[e] = 0.f;
-                    if (m >= sb && m < se) {
-                        const float* vp = seg.v + (int64_t)m * seg.vstride + jb + j;
-                        const f32x4 q0 = *reinterpret_cast<const f32x4*>(vp);
-                        const f32x4 q1 = *reinterpret_cast<const f32x4*>(vp + 4);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            vv[e] = jb + j + e < r ? q0[e] : 0.f;
-                            vv[4 + e] = jb + j + 4 + e < r ? q1[e] : 0.f;
-                        }
-                    }
-                    u32x4 hi, lo;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float a0 = gamma * vv[2 * i], a1 = gamma * vv[2 * i + 1];
-                        const uint32_t h0 = f32_to_bf16(a0), h1 = f32_to_bf16(a1);
-                        hi[i] = h0 | (h1 << 16);
-                        lo[i] = pack_bf16(a0 - __uint_as_float(h0 << 16), a1 - __uint_as_float(h1 << 16));
-                    }
-                    *reinterpret_cast<u32x4*>(&vh[ml * LDJ + j]) = hi;
-                    *reinterpret_cast<u32x4*>(&vl[ml * LDJ + j]) = lo;
-                }
-                __syncthreads();
-                const int j0 = 8 * lg;
-                u32x4 vhi[FM], vlo[FM];
-#pragma unroll
-                for (int b = 0; b < FM; ++b) {
-                    vhi[b] = *reinterpret_cast<const u32x4*>(&vh[(wm * WTM + b * 16 + li) * LDJ + j0]);
-                    vlo[b] = *reinterpret_cast<const u32x4*>(&vl[(wm * WTM + b * 16 + li) * LDJ + j0]);
-                }
-#pragma unroll
-                for (int a = 0; a < FN; ++a) {
-                    const u32x4 bfr = *reinterpret_cast<const u32x4*>(&bt[(wn * WTN + a * 16 + li) * LDJ + j0]);
-#pragma unroll
-                    for (int b = 0; b < FM; ++b) {
-                        acc[a][b] = mma_step(bfr, vhi[b], acc[a][b], bf16_t{});
-                        acc[a][b] = mma_step(bfr, vlo[b], acc[a][b], bf16_t{});
-                    }
-                }
-            }
-        }
+        uint16_t* vl = S > 2 ? reinterpret_cast<uint16_t*>(lds2) : vh + BM * kExpandRow;
+        expand_segments<BM, BN, WM, WN>(seg, m0, n0, N, reinterpret_cast<uint16_t*>(lds0), vh, vl, acc);
     }
 
     // lane holds D[n = 4*lg + i][m = li] of each 16x16 block
