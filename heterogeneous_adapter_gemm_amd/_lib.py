@@ -97,6 +97,21 @@ class lora_kv_rows(ctypes.Structure):
                                       "v_out_stride")]
 
 
+class lora_norm_rows(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int64), ("d", ctypes.c_int32), ("eps", ctypes.c_float)] + [
+        (n, _VP) for n in ("x", "residual", "weight", "sum_out", "y", "held", "code", "scale")] + [
+        (n, ctypes.c_int64) for n in ("x_stride", "residual_stride", "sum_stride", "y_stride", "held_stride")]
+
+
+class lora_act_rows(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int64), ("d", ctypes.c_int32), ("act", ctypes.c_int32)] + [
+        (n, _VP) for n in ("x", "gate", "y", "held", "code", "scale")] + [
+        (n, ctypes.c_int64) for n in ("x_stride", "gate_stride", "y_stride", "held_stride")]
+
+
+LORA_ACT_NONE, LORA_ACT_SILU, LORA_ACT_GELU, LORA_ACT_GELU_TANH = range(4)
+ACTS = {"none": LORA_ACT_NONE, "silu": LORA_ACT_SILU, "gelu": LORA_ACT_GELU, "gelu_tanh": LORA_ACT_GELU_TANH}
+
 _SIGS = {
     "lora_pool_meta_bytes": [ctypes.POINTER(lora_pool_desc), _I64P],
     "lora_pool_create": [ctypes.POINTER(lora_pool_desc), ctypes.POINTER(_VP)],
@@ -129,6 +144,11 @@ _SIGS = {
     "lora_linear_fp8": [_VP, _VP, ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP],
     "base_gemm_w4": [_VP, _VP, _VP, _VP, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _VP],
     "lora_linear_w4": [_VP, _VP, ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP, ctypes.c_int32, _VP, _VP],
+    "rows_norm_i8": [ctypes.POINTER(lora_norm_rows), _VP],
+    "rows_act_i8": [ctypes.POINTER(lora_act_rows), _VP],
+    "base_gemm_i8": [_VP, _VP, _VP, _VP, _VP, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _VP],
+    "base_gated_i8": [_VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int32, _VP, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _VP],
+    "lora_linear_i8": [_VP, _VP, ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP, _VP, _VP],
     "lora_kv_pages_per_block": [_VP, ctypes.c_int32, ctypes.c_int32, _I32P],
     "lora_kv_workspace_bytes": [ctypes.POINTER(lora_kv_batch), _I64P],
     "lora_kv_append": [_VP, ctypes.POINTER(lora_kv_batch), ctypes.POINTER(lora_kv_rows), _VP, ctypes.c_int32,
@@ -504,6 +524,112 @@ def lora_linear_w4(pool: Pool, plan: Plan, layer: int, proj: int, x, w0_code, w0
     _on_gpu(stream, lambda st: _check(library().lora_linear_w4(pool.handle, plan.handle, layer, proj, _addr(x),
                                                                _addr(w0_code), _addr(w0_scale), group, _addr(y), st),
                                       "lora_linear_w4"), pool.pages, x, w0_code, w0_scale, y)
+
+
+_row_types = None
+
+
+def _rows(name: str, t, n: int, d: int, device: int):
+    """Address and row stride of bf16 rows [n, d] on a GPU (None: NULL)."""
+    if t is None:
+        return None, 0
+    shape, st = t.shape, t.stride()
+    if t.dtype is not _row_types[0] or t.get_device() != device or len(shape) != 2 or shape[0] != n or shape[1] != d or st[1] != 1:
+        raise ValueError(f"{name}: bfloat16 rows [{n}, {d}], contiguous along a row, on the GPU of x are needed")
+    return t.data_ptr(), st[0] if n > 1 else d
+
+
+def _form(code, scale, n: int, d: int, device: int):
+    """Addresses of the codes [n, d] and scales [n] of rows (both None: NULL)."""
+    if code is None and scale is None:
+        return None, None
+    if code is None or scale is None or code.dtype is not _row_types[1] or scale.dtype is not _row_types[2] or \
+            code.get_device() != device or scale.get_device() != device or tuple(code.shape) != (n, d) or \
+            tuple(scale.shape) != (n,) or not code.is_contiguous() or not scale.is_contiguous():
+        raise ValueError(f"code and scale: contiguous int8 [{n}, {d}] and float32 [{n}] on the GPU of x, together")
+    return code.data_ptr(), scale.data_ptr()
+
+
+def _rows_call(name: str, x, stream, rows) -> None:
+    import torch
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: x must be on a GPU")
+    st = current_stream(dev) if stream is None else _stream(stream)
+    if torch.cuda.current_device() == dev:
+        _check(getattr(library(), name)(rows, st), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(getattr(library(), name)(rows, st), name)
+
+
+def _row_shape(x):
+    global _row_types
+    if _row_types is None:
+        import torch
+        _row_types = torch.bfloat16, torch.int8, torch.float32
+    if x.dim() != 2:
+        raise ValueError(f"x: rows [n, d] are needed, not {tuple(x.shape)}")
+    return x.shape[0], x.shape[1], x.get_device()
+
+
+def rows_norm_i8(x, weight, eps: float, residual=None, sum_out=None, y=None, code=None, scale=None, held=None,
+                 stream=None) -> None:
+    """Norm of bf16 rows x (+ residual) [n, d] with the weight [d]: y, and the 8-bit form code, scale, held."""
+    n, d, dev = _row_shape(x)
+    if weight.dtype is not _row_types[0] or tuple(weight.shape) != (d,) or weight.get_device() != dev or \
+            not weight.is_contiguous():
+        raise ValueError(f"weight: contiguous bfloat16 [{d}] on the GPU of x is needed")
+    xp, xs = _rows("x", x, n, d, dev)
+    rp, rs = _rows("residual", residual, n, d, dev)
+    sp, ss = _rows("sum_out", sum_out, n, d, dev)
+    yp, ys = _rows("y", y, n, d, dev)
+    hp, hs = _rows("held", held, n, d, dev)
+    cp, fp = _form(code, scale, n, d, dev)
+    _rows_call("rows_norm_i8", x, stream, lora_norm_rows(n, d, eps, xp, rp, weight.data_ptr(), sp, yp, hp, cp, fp, xs, rs,
+                                                         ss, ys, hs))
+
+
+def rows_act_i8(x, gate=None, act="none", y=None, code=None, scale=None, held=None, stream=None) -> None:
+    """a = act(gate) * x (x alone with "none") of bf16 rows [n, d]: y, and its 8-bit form code, scale, held.
+    act: "none", "silu", "gelu", "gelu_tanh" or a LORA_ACT_* number."""
+    n, d, dev = _row_shape(x)
+    if isinstance(act, str):
+        if act not in ACTS:
+            raise ValueError(f"act {act!r}: one of {', '.join(ACTS)}")
+        act = ACTS[act]
+    xp, xs = _rows("x", x, n, d, dev)
+    gp, gs = _rows("gate", gate, n, d, dev)
+    yp, ys = _rows("y", y, n, d, dev)
+    hp, hs = _rows("held", held, n, d, dev)
+    cp, fp = _form(code, scale, n, d, dev)
+    _rows_call("rows_act_i8", x, stream, lora_act_rows(n, d, act, xp, gp, yp, hp, cp, fp, xs, gs, ys, hs))
+
+
+def base_gemm_i8(x_code, x_scale, w0_code, w0_scale, y, M: int, N: int, K: int, stream=None) -> None:
+    _on_gpu(stream, lambda st: _check(library().base_gemm_i8(_addr(x_code), _addr(x_scale), _addr(w0_code), _addr(w0_scale),
+                                                             _addr(y), M, N, K, st), "base_gemm_i8"),
+            x_code, x_scale, w0_code, w0_scale, y)
+
+
+def base_gated_i8(x_code, x_scale, wg_code, wg_scale, wu_code, wu_scale, y, M: int, N: int, K: int, act="silu",
+                  stream=None) -> None:
+    """y = act(gate) * up of one feed-forward block; act: "silu", "gelu", "gelu_tanh" or a LORA_ACT_* number."""
+    if isinstance(act, str):
+        if act not in ACTS:
+            raise ValueError(f"act {act!r}: one of {', '.join(ACTS)}")
+        act = ACTS[act]
+    _on_gpu(stream, lambda st: _check(library().base_gated_i8(_addr(x_code), _addr(x_scale), _addr(wg_code), _addr(wg_scale),
+                                                              _addr(wu_code), _addr(wu_scale), act, _addr(y), M, N, K, st),
+                                      "base_gated_i8"), x_code, x_scale, wg_code, wg_scale, wu_code, wu_scale, y)
+
+
+def lora_linear_i8(pool: Pool, plan: Plan, layer: int, proj: int, x, x_code, x_scale, w0_code, w0_scale, y,
+                   stream=None) -> None:
+    _on_gpu(stream, lambda st: _check(library().lora_linear_i8(pool.handle, plan.handle, layer, proj, _addr(x),
+                                                               _addr(x_code), _addr(x_scale), _addr(w0_code),
+                                                               _addr(w0_scale), _addr(y), st), "lora_linear_i8"),
+            pool.pages, x, x_code, x_scale, w0_code, w0_scale, y)
 
 
 def lora_kv_pages_per_block(pool: Pool, n_kv_heads: int, head_dim: int) -> int:

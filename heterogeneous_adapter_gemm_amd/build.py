@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libhagemm.so")
 SOURCES = ["pool.cpp", "engine.cpp", "lora_kernels.hip", "gemm_kernels.hip", "w8_kernels.hip", "w4_kernels.hip",
-           "kv.cpp", "kv_kernels.hip", "probe.hip"]
+           "kv.cpp", "kv_kernels.hip", "i8.cpp", "i8_kernels.hip", "rows_kernels.hip", "probe.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

@@ -23,6 +23,7 @@
 #include <unordered_map>
 #include <vector>
 
+#include "i8.h"
 #include "internal.h"
 #include "lora_gemm.h"
 
@@ -1297,9 +1298,14 @@ namespace {
 // n projections of one layer that share x (n = 1: one lora_linear call): their shrinks run in
 // shared launches, then each projection's base GEMM and expand
 // w0_scale NULL: w0s are in the pool's type; else one projection whose base is FP8 (w4_group 0,
-// fp32 scales) or 4-bit (w4_group: k per scale and zero).
+// fp32 scales), 4-bit (w4_group: k per scale and zero) or 8-bit integers (i8: the rows' codes and scales).
+struct I8Rows {
+    const int8_t* code;
+    const float* scale;
+};
 int linear_impl(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t n, const int32_t* projs, const void* x,
-                const void* const* w0s, const void* w0_scale, int32_t w4_group, void* const* ys, void* stream) {
+                const void* const* w0s, const void* w0_scale, int32_t w4_group, void* const* ys, void* stream,
+                const I8Rows* i8 = nullptr) {
     if (!p || !plan || plan->pool != p) return fail(LORA_EINVAL, "plan does not belong to this pool");
     if (p->host_only) return fail(LORA_EINVAL, "host-only pool: no device work");
     if (n < 1 || !projs || !w0s || !ys) return fail(LORA_EINVAL, "no projections");
@@ -1410,7 +1416,7 @@ int linear_impl(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t n, c
     }
     hipError_t e = hipSuccess;
     const int dt = p->dtype;
-    const bool w4 = w0_scale != nullptr && w4_group != 0, fp8 = w0_scale != nullptr && !w4;
+    const bool w4 = w0_scale != nullptr && w4_group != 0, fp8 = w0_scale != nullptr && !w4 && !i8;
     const float* w8_scale = static_cast<const float*>(w0_scale);
     if (fp8 && (dt != LORA_BF16 || !gemm_w8_ok(T, a.d_out, a.d_in) || (uintptr_t)w0_scale % 16))
         return fail(LORA_EINVAL, "FP8 base: needs a bf16 pool, d_in a multiple of 128, d_out of 4, a 16-byte aligned "
@@ -1418,14 +1424,29 @@ int linear_impl(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t n, c
     if (w4 && (dt != LORA_BF16 || !gemm_w4_ok(T, a.d_out, a.d_in, w4_group) || (uintptr_t)w0_scale % 16))
         return fail(LORA_EINVAL, "4-bit base: needs a bf16 pool, a group of 32, 64 or 128, d_in a multiple of 128, d_out "
                                  "of 4, a 16-byte aligned w0_scale and 32-bit byte offsets");
+    if (i8 && (dt != LORA_BF16 || !gemm_i8_ok(T, a.d_out, a.d_in)))
+        return fail(LORA_EINVAL, "8-bit base: needs a bf16 pool, d_in a multiple of 16 up to %lld", (long long)kI8MaxK);
     const bool any = plan->n_groups > 0 || plan->n_tiles > 0;
     float* ybase = any ? reinterpret_cast<float*>(base + L.ybase_bytes_off) : nullptr;
     const int32_t* rs = any ? I(L.row_slot) : nullptr;
     // decode batches: the base GEMM and the BGMV shrink share one launch
     const bool gemm_done = w0 && a.n_tiles == 0 &&
-                           (w4    ? gemm_w4_shrink_fits(T, a.d_out, a.d_in, w4_group, a.n_su)
+                           (i8    ? gemm_i8_shrink_fits(T, a.d_out, a.d_in, a.n_su)
+                            : w4  ? gemm_w4_shrink_fits(T, a.d_out, a.d_in, w4_group, a.n_su)
                             : fp8 ? gemm_w8_shrink_fits(T, a.d_out, a.d_in, a.n_su)
                                   : gemm_shrink_fits(dt, T, a.n_su));
+    I8Args ia{};
+    if (i8) {
+        ia.x = i8->code;
+        ia.xs = i8->scale;
+        ia.w = w0;
+        ia.ws = w8_scale;
+        ia.y = y;
+        ia.ybase = ybase;
+        ia.M = T;
+        ia.N = a.d_out;
+        ia.K = a.d_in;
+    }
     const PlanStage& ps = p->pstage[plan->stage];
     if (first && !gemm_done) {
         // (a batch without adapter rows reads no index)
@@ -1466,6 +1487,10 @@ int linear_impl(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t n, c
             const void* cps = first ? ps.host_dev : nullptr;
             void* cpd = first ? base : nullptr;
             const int64_t cpn = first ? plan->words : 0;
+            if (i8) {
+                ia.row_slot = rsh;
+                return launch_gemm_i8_shrink(ia, raw_mask, ah, cps, cpd, cpn, st);
+            }
             return w4    ? launch_gemm_w4_shrink(x, w0, w0_scale, w4_group, y, T, a.d_out, a.d_in, rsh, raw_mask, ybase,
                                                  ah, cps, cpd, cpn, st)
                    : fp8 ? launch_gemm_w8_shrink(x, w0, w8_scale, y, T, a.d_out, a.d_in, rsh, raw_mask, ybase, ah, cps,
@@ -1509,6 +1534,10 @@ int linear_impl(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t n, c
             // rows with an adapter keep the unrounded base for their expand: one rounding in total
             const LoraArgs* seg = plan->n_tiles > 0 ? &ai : nullptr;
             e = timed_launch(p, LORA_K_GEMM, st, [&] {
+                if (i8) {
+                    ia.row_slot = rs;
+                    return launch_gemm_i8(ia, seg, &fused, st);
+                }
                 return w4  ? launch_gemm_w4(x, wi, w0_scale, w4_group, yi, T, ai.d_out, ai.d_in, rs, ybase_i, st)
                        : fp8 ? launch_gemm_w8(x, wi, w8_scale, yi, T, ai.d_out, ai.d_in, rs, ybase_i, st)
                            : launch_gemm(dt, x, wi, yi, T, ai.d_out, ai.d_in, rs, ybase_i, seg, &fused, st);
@@ -1557,6 +1586,19 @@ int lora_linear_w4(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t p
     if (!w0_code || !w0_scale) return fail(LORA_EINVAL, "w0_code and w0_scale are required");
     if (group != 32 && group != 64 && group != 128) return fail(LORA_EINVAL, "group must be 32, 64 or 128");
     return linear_impl(p, plan, layer, 1, &proj, x, &w0_code, w0_scale, group, &y, stream);
+}
+
+int lora_linear_i8(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t proj, const void* x, const int8_t* x_code,
+                   const float* x_scale, const int8_t* w0_code, const float* w0_scale, void* y, void* stream) {
+    if (!w0_code || !w0_scale) return fail(LORA_EINVAL, "w0_code and w0_scale are required");
+    if (plan && plan->T_pre + plan->T_dec > 0) {
+        if (!x_code || !x_scale) return fail(LORA_EINVAL, "x_code and x_scale are required");
+        if ((uintptr_t)x_code % 16 || (uintptr_t)x_scale % 16 || (uintptr_t)w0_scale % 16)
+            return fail(LORA_EINVAL, "x_code, x_scale and w0_scale must be 16-byte aligned");
+    }
+    const I8Rows i8{x_code, x_scale};
+    const void* w0 = w0_code;
+    return linear_impl(p, plan, layer, 1, &proj, x, &w0, w0_scale, 0, &y, stream, &i8);
 }
 
 int lora_linear_decode(lora_pool* p, int32_t layer, int32_t proj, const void* x, const void* w0, void* y,

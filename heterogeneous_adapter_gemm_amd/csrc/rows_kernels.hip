@@ -1,0 +1,279 @@
+// Rows of a layer and their 8-bit form (gfx950).
+//
+// A row p of d values has the 8-bit form scale * code: m = max |p|, code_j the integer nearest to
+// 127 p_j / m (ties to even), scale = m / 127 (the norm: m r / 127).  The codes are exact: with p and m
+// scaled by the power of two that brings m to [1, 2), 127 p has at most 23 significant bits (p is a
+// product of two bf16 numbers, or one), a candidate q from a product with 127 / m is at most one off,
+// and e = 127 p - q m fits 24 bits, so that one fma and a comparison of |e| with m / 2 settle it.
+//
+// The norm: h = x + residual rounded to bf16 (the residual stream as it is kept), p = h w, r = 1 /
+// sqrt(mean h^2 + eps), y = p r.  p is exact in fp32 and r is common to a row, so the codes depend on
+// neither the order of the sum of squares nor on r.
+//
+// Each row is read once: a workgroup (rows of up to 1024 values: a wave) holds it in registers from its
+// loads to its stores, with one reduction in between.  The kernels are bound by memory: 16-byte loads and
+// stores of consecutive lanes.
+#include "act_device.h"
+#include "common.h"
+#include "rows.h"
+
+namespace hagemm {
+namespace {
+
+// bits of |v|; their order is that of the magnitudes, with NaN above infinity above all numbers
+__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// what the 8-bit form of a row needs from its greatest magnitude (bits)
+struct Form {
+    float m, inv;   // scaled to [1, 2); 127 / m
+    int e;          // its exponent
+    bool zero;      // all codes 0: the row is zero, or holds what is no number
+    __device__ __forceinline__ explicit Form(uint32_t bits) {
+        zero = bits == 0 || bits >= 0x7F800000u;
+        const float v = zero ? 1.f : __uint_as_float(bits);
+        e = 1 - __builtin_amdgcn_frexp_expf(v);
+        m = ldexpf(v, e);
+        inv = 127.f / m;
+    }
+    // the code of p, |p| <= m: a whole number
+    __device__ __forceinline__ float code(float p) const {
+        const float t = __builtin_amdgcn_ldexpf(p, e);
+        const float q = rintf(t * inv);
+        const float rest = fmaf(-q, m, 127.f * t), far = fabsf(rest), half = 0.5f * m;
+        const bool odd = ((int)q & 1) != 0;
+        const float r = (far > half || (far == half && odd)) ? q + copysignf(1.f, rest) : q;
+        return zero ? 0.f : r;
+    }
+};
+
+// sum and greatest bits over the row's threads: a wave, or the workgroup
+template <bool WAVE>
+__device__ __forceinline__ void reduce(float& s, uint32_t& m) {
+#pragma unroll
+    for (int k = 32; k >= 1; k >>= 1) {
+        s += __shfl_xor(s, k, 64);
+        m = max(m, (uint32_t)__shfl_xor((int)m, k, 64));
+    }
+    if constexpr (!WAVE) {
+        __shared__ float ps[16];
+        __shared__ uint32_t pm[16];
+        const int wave = threadIdx.x >> 6, n = blockDim.x >> 6;
+        if ((threadIdx.x & 63) == 0) {
+            ps[wave] = s;
+            pm[wave] = m;
+        }
+        __syncthreads();
+        s = 0.f;
+        m = 0;
+        for (int i = 0; i < n; ++i) {
+            s += ps[i];
+            m = max(m, pm[i]);
+        }
+    }
+}
+
+__device__ __forceinline__ bf16_t* row_of(void* p, int64_t row, int64_t stride) { return static_cast<bf16_t*>(p) + row * stride; }
+__device__ __forceinline__ const bf16_t* row_of(const void* p, int64_t row, int64_t stride) {
+    return static_cast<const bf16_t*>(p) + row * stride;
+}
+
+// codes and held values of the eight values p of vector v of a row
+__device__ __forceinline__ void put_form(const RowsArgs& a, int64_t row, int v, const float (&p)[8], const Form& f, float scale) {
+    float q[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = f.code(p[e]);
+    if (a.code) {
+        u32x2 c;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            uint32_t b = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b |= ((uint32_t)(int)q[4 * w + e] & 0xFFu) << (8 * e);
+            c[w] = b;
+        }
+        *reinterpret_cast<u32x2*>(a.code + row * a.d + v * 8) = c;
+    }
+    if (a.held) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] *= scale;
+        st16(row_of(a.held, row, a.held_stride) + v * 8, pack(q, bf16_t{}));
+    }
+}
+
+// NV vectors of 8 values a thread; WAVE: a wave a row and four rows a workgroup, else a workgroup a row
+template <int NV, bool WAVE>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void rows_norm_kernel(RowsArgs a) {
+    const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    if (WAVE && row >= a.n_rows) return;
+    const int t = WAVE ? threadIdx.x & 63 : threadIdx.x, nt = WAVE ? 64 : blockDim.x, vecs = a.d >> 3;
+    const u32x4 none = {0u, 0u, 0u, 0u};
+    u32x4 h[NV], w[NV];
+    const bf16_t* x = row_of(a.x, row, a.x_stride);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = t + i * nt;
+        h[i] = v < vecs ? ld16(x + v * 8) : none;
+        w[i] = v < vecs ? ld16(static_cast<const bf16_t*>(a.weight) + v * 8) : none;
+    }
+    if (a.other) {
+        const bf16_t* r = row_of(a.other, row, a.other_stride);
+        u32x4 rv[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = t + i * nt;
+            rv[i] = v < vecs ? ld16(r + v * 8) : none;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float p[8], q[8];
+            unpack(h[i], p, bf16_t{});
+            unpack(rv[i], q, bf16_t{});
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] += q[e];
+            h[i] = pack(p, bf16_t{});
+            const int v = t + i * nt;
+            if (a.sum_out && v < vecs) st16(row_of(a.sum_out, row, a.sum_stride) + v * 8, h[i]);
+        }
+    }
+    float ss = 0.f;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float p[8], g[8];
+        unpack(h[i], p, bf16_t{});
+        unpack(w[i], g, bf16_t{});
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            ss = fmaf(p[e], p[e], ss);
+            m = max(m, mag(p[e] * g[e]));
+        }
+    }
+    reduce<WAVE>(ss, m);
+    // squares past fp32's range leave no norm: the row is NaN, as one that holds an infinity or NaN is
+    const float r = ss < INFINITY ? 1.f / sqrtf(ss / (float)a.d + a.eps) : NAN;
+    const Form f(m);
+    const float scale = m < 0x7F800000u ? __uint_as_float(m) * r / 127.f : NAN;
+    if (a.scale && t == 0) a.scale[row] = scale;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = t + i * nt;
+        if (v >= vecs) break;
+        float p[8], g[8];
+        unpack(h[i], p, bf16_t{});
+        unpack(w[i], g, bf16_t{});
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] *= g[e];
+        if (a.code || a.held) put_form(a, row, v, p, f, scale);
+        if (a.y) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] *= r;
+            st16(row_of(a.y, row, a.y_stride) + v * 8, pack(p, bf16_t{}));
+        }
+    }
+}
+
+template <int NV, bool WAVE, int ACT>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void rows_act_kernel(RowsArgs a) {
+    const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    if (WAVE && row >= a.n_rows) return;
+    const int t = WAVE ? threadIdx.x & 63 : threadIdx.x, nt = WAVE ? 64 : blockDim.x, vecs = a.d >> 3;
+    const u32x4 none = {0u, 0u, 0u, 0u};
+    u32x4 h[NV], gv[NV];
+    const bf16_t* x = row_of(a.x, row, a.x_stride);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = t + i * nt;
+        h[i] = v < vecs ? ld16(x + v * 8) : none;
+        if constexpr (ACT != kActNone) gv[i] = v < vecs ? ld16(row_of(a.other, row, a.other_stride) + v * 8) : none;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float p[8];
+        if constexpr (ACT != kActNone) {
+            float g[8];
+            unpack(h[i], p, bf16_t{});
+            unpack(gv[i], g, bf16_t{});
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] *= activate<ACT>(g[e]);
+            h[i] = pack(p, bf16_t{});
+        }
+        unpack(h[i], p, bf16_t{});
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max(m, mag(p[e]));
+    }
+    if (a.y) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = t + i * nt;
+            if (v < vecs) st16(row_of(a.y, row, a.y_stride) + v * 8, h[i]);
+        }
+    }
+    if (!a.code && !a.held) return;
+    float unused = 0.f;
+    reduce<WAVE>(unused, m);
+    const Form f(m);
+    const float scale = m < 0x7F800000u ? __uint_as_float(m) / 127.f : NAN;
+    if (a.scale && t == 0) a.scale[row] = scale;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = t + i * nt;
+        if (v >= vecs) break;
+        float p[8];
+        unpack(h[i], p, bf16_t{});
+        put_form(a, row, v, p, f, scale);
+    }
+}
+
+// Threads a row: a wave for rows of up to 1024 values; else the fewest vectors a thread that leave a
+// workgroup of at most 512 threads (1024 for the widest rows).
+template <class Go>
+hipError_t by_width(const RowsArgs& a, Go go) {
+    if (a.n_rows < 1 || a.d < 8 || a.d % 8 || a.d > kMaxRowWidth) return hipErrorInvalidValue;
+    const int vecs = a.d / 8;
+    auto waves = [&](int nv) { return dim3((vecs + nv * 64 - 1) / (nv * 64) * 64); };
+    const dim3 rows(a.n_rows), fours((a.n_rows + 3) / 4), four(256);
+    if (vecs <= 64) go.template operator()<1, true>(fours, four);
+    else if (vecs <= 128) go.template operator()<2, true>(fours, four);
+    else if (vecs <= 512) go.template operator()<1, false>(rows, waves(1));
+    else if (vecs <= 1024) go.template operator()<2, false>(rows, waves(2));
+    else if (vecs <= 1536) go.template operator()<3, false>(rows, waves(3));
+    else if (vecs <= 2048) go.template operator()<4, false>(rows, waves(4));
+    else go.template operator()<8, false>(rows, waves(8));
+    return hipGetLastError();
+}
+
+struct GoNorm {
+    const RowsArgs& a;
+    hipStream_t s;
+    template <int NV, bool WAVE>
+    void operator()(dim3 grid, dim3 block) const {
+        hipLaunchKernelGGL((rows_norm_kernel<NV, WAVE>), grid, block, 0, s, a);
+    }
+};
+
+template <int ACT>
+struct GoAct {
+    const RowsArgs& a;
+    hipStream_t s;
+    template <int NV, bool WAVE>
+    void operator()(dim3 grid, dim3 block) const {
+        hipLaunchKernelGGL((rows_act_kernel<NV, WAVE, ACT>), grid, block, 0, s, a);
+    }
+};
+
+}  // namespace
+
+hipError_t launch_rows_norm(const RowsArgs& a, hipStream_t s) { return by_width(a, GoNorm{a, s}); }
+
+hipError_t launch_rows_act(const RowsArgs& a, int act, hipStream_t s) {
+    switch (act) {
+        case kActNone: return by_width(a, GoAct<kActNone>{a, s});
+        case kActSilu: return by_width(a, GoAct<kActSilu>{a, s});
+        case kActGelu: return by_width(a, GoAct<kActGelu>{a, s});
+        case kActGeluTanh: return by_width(a, GoAct<kActGeluTanh>{a, s});
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace hagemm

@@ -200,6 +200,10 @@ class DevicePool:
     def linear_w4(self, plan: L.Plan, layer: int, proj: int, x, w0_code, w0_scale, group: int, y, stream=None) -> None:
         L.lora_linear_w4(self.pool, plan, layer, proj, x, w0_code, w0_scale, group, y, stream)
 
+    def linear_i8(self, plan: L.Plan, layer: int, proj: int, x, x_code, x_scale, w0_code, w0_scale, y, stream=None) -> None:
+        """x: the bf16 rows the adapters read; x_code, x_scale: the 8-bit form of them that the base reads."""
+        L.lora_linear_i8(self.pool, plan, layer, proj, x, x_code, x_scale, w0_code, w0_scale, y, stream)
+
     # -- keys and values in the pages ----------------------------------------------
     def kv_pages_per_block(self, n_kv_heads: int, head_dim: int) -> int:
         """Pages of 16 tokens' keys and values in one layer."""

@@ -395,6 +395,84 @@ int lora_linear_w4(lora_pool* pool, const lora_plan* plan, int32_t layer, int32_
                    const void* w0_code, const void* w0_scale, int32_t group, void* y, void* stream);
 
 /*
+ * 8-bit integers ("Multi-LoRA serving ...", Interaction with how the adapters were trained: a base served
+ * quantized with 16-bit adapters): rows and base weight in int8 codes, a scale a row and a scale an output
+ * channel, so that the base product runs on the integer matrix operations.  The adapters' path keeps the
+ * bf16 rows.
+ *
+ * The 8-bit form of a row p of d values is scale * code: m = max |p|, code_j the integer in -127..127 nearest to
+ * 127 p_j / m (ties to even), exactly; scale = m / 127 in fp32.  A row of zeros has scale 0 and codes 0.  A row
+ * that holds an infinity or NaN has scale NaN and codes 0, so that it reads back as NaN.  `held` is what the
+ * codes stand for: scale * code rounded to bf16.
+ *
+ * Rows are bf16, 16-byte aligned, with strides in elements (multiples of 8, at least d); code is [n_rows][d]
+ * (16-byte aligned), scale [n_rows].  d is a multiple of 8 up to 65536.  An output may lie where an input of the
+ * call does if it has that input's address and stride; otherwise inputs and outputs must not overlap.
+ */
+enum { LORA_ACT_NONE = 0, LORA_ACT_SILU = 1, LORA_ACT_GELU = 2, LORA_ACT_GELU_TANH = 3 };
+
+typedef struct lora_norm_rows {
+    int64_t n_rows;
+    int32_t d;
+    float eps;                      /* > 0 */
+    const void *x, *residual;       /* residual NULL: none */
+    const void* weight;             /* bf16 [d], 16-byte aligned */
+    void *sum_out, *y, *held;       /* each may be NULL (sum_out needs a residual) */
+    int8_t* code;                   /* code and scale may be NULL, together */
+    float* scale;
+    int64_t x_stride, residual_stride, sum_stride, y_stride, held_stride;
+} lora_norm_rows;
+
+/* Root-mean-square norm of rows, with the residual's addition before it and the 8-bit form after it:
+ *   h = x + residual, rounded to bf16 (sum_out; without a residual h = x)
+ *   p = h * weight (exact in fp32),  r = 1 / sqrt(mean h^2 + eps)
+ *   y = p r, rounded to bf16 once;  code and scale the 8-bit form of p r, where the codes are those of p (r is the
+ *   row's own factor and cancels): they depend on no rounding of y or r.  scale = max |p| r / 127.
+ * Sums are fp32: a row whose sum of squares passes fp32's range is NaN, as one that holds an infinity or NaN.
+ * n_rows = 0 is a no-op.  Errors: EINVAL, EHIP. */
+int rows_norm_i8(const lora_norm_rows* rows, void* stream);
+
+typedef struct lora_act_rows {
+    int64_t n_rows;
+    int32_t d;
+    int32_t act;                    /* LORA_ACT_* */
+    const void *x, *gate;           /* gate NULL with LORA_ACT_NONE, and only with it */
+    void *y, *held;                 /* each may be NULL */
+    int8_t* code;                   /* code and scale may be NULL, together */
+    float* scale;
+    int64_t x_stride, gate_stride, y_stride, held_stride;
+} lora_act_rows;
+
+/* Rows on their way into a projection: a = act(gate) * x in fp32, rounded to bf16 (y), or a = x without a gate;
+ * code and scale the 8-bit form of a.  silu(v) = v / (1 + e^-v), gelu(v) = v (1 + erf(v / sqrt 2)) / 2, gelu_tanh
+ * the same with tanh(sqrt(2 / pi) (v + 0.044715 v^3)) in erf's place.  gate and x may be the halves of one
+ * projection's rows (strides).  n_rows = 0 is a no-op.  Errors: EINVAL, EHIP. */
+int rows_act_i8(const lora_act_rows* rows, void* stream);
+
+/* The base product in 8-bit integers: y[m][n] = x_scale[m] w0_scale[n] sum_k x_code[m][k] w0_code[n][k], the sum
+ * exact in 32-bit integers, then fp32, rounded to bf16 once.  x_code [M][K], x_scale fp32 [M], w0_code [N][K],
+ * w0_scale fp32 [N], y bf16 [M][N].  Codes may be anything of int8.  A row (or channel) whose scale is NaN or
+ * infinite is NaN or infinite throughout (NaN where its sum is 0).  Requires N % 4 == 0, K % 16 == 0, K <= 131056,
+ * M and N <= 2^22, 16-byte aligned pointers.  M = 0 is a no-op.  Errors: EINVAL, EHIP. */
+int base_gemm_i8(const int8_t* x_code, const float* x_scale, const int8_t* w0_code, const float* w0_scale, void* y, int64_t M,
+                 int64_t N, int64_t K, void* stream);
+
+/* The gated product of a feed-forward block whose gate and up projections have no adapters, in one launch (two
+ * where a long batch's last round of tiles is cut up): y = act(g) u, g and u the products of the rows with the
+ * two weights as base_gemm_i8 computes them, unrounded; y is rounded to bf16 once.  act: LORA_ACT_SILU, _GELU or
+ * _GELU_TANH (with adapters: two lora_linear_i8 and rows_act_i8).  Requirements and errors as base_gemm_i8. */
+int base_gated_i8(const int8_t* x_code, const float* x_scale, const int8_t* wg_code, const float* wg_scale, const int8_t* wu_code,
+                  const float* wu_scale, int32_t act, void* y, int64_t M, int64_t N, int64_t K, void* stream);
+
+/* lora_linear with an 8-bit base (bf16 pool): y = base + delta, the base as in base_gemm_i8 from x_code [T][d_in]
+ * and x_scale [T], the delta lora_linear's from the bf16 rows x (what the codes were made from, or their held
+ * rows, as the adapters were trained); rows with an adapter are rounded once, rows without one are base_gemm_i8's
+ * bit for bit.  A call to be captured is not its plan's first one (which brings the plan's index to the device).
+ * Errors as lora_linear, and EINVAL when the pool is not bf16 or the shapes break base_gemm_i8's requirements. */
+int lora_linear_i8(lora_pool* pool, const lora_plan* plan, int32_t layer, int32_t proj, const void* x, const int8_t* x_code,
+                   const float* x_scale, const int8_t* w0_code, const float* w0_scale, void* y, void* stream);
+
+/*
  * Keys and values in the pool's KV pages, 4 bits each ("S-LoRA: Serving
  * Thousands of Concurrent LoRA Adapters", Unified paging: KV blocks share the
  * adapters' pages).  lora_kv_append puts a step's new rows there, turning
