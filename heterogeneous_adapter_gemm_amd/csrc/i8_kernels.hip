@@ -13,10 +13,12 @@
 //    16 FM rows x 16 FN columns (gated: 8 FN of each weight); wave v takes every fourth slice of 128 K, streams
 //    both operands' rows of its slices through an LDS ring of its own, and holds a whole tile of partial sums.
 //    So no wave waits for another until the end, where the four partial tiles are added in LDS.
-//  * i8_long_kernel (more rows): bound by the matrix operations and the feed of the tiles.  256 x 256 (or 192 x
-//    256) tiles, eight waves, four stages of 64 K, fragments read one step ahead; the prefill segments'
+//  * i8_long_kernel (more rows): bound by the matrix operations' power (below).  256 x 256 (or 192 x 256) tiles, eight
+//    waves, steps of 128 K, rings of two and three stages, fragments read half a step ahead; the prefill segments'
 //    expand in the epilogue.
 //
+// Rows are loaded 128 bytes at a time, whole cache lines: a compute unit has about 512 lines on their way at once, and
+// with 64-byte rows (half a line each) it draws 57 GB/s from the L2 instead of 112.
 // Both load straight into LDS, by buffers of a tile's own rows of one matrix: rows past M or N read as zeros, no
 // offset passes 32 bits, and columns past K are asked for past the buffer's end and read as zeros too.
 #include <type_traits>
@@ -37,7 +39,7 @@ __device__ __forceinline__ i32x4 mma_i8(const u32x4& a, const u32x4& b, i32x4 c)
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
 
-// past the end of every buffer below (each is at most 64 rows: 8 MiB)
+// past the end of every buffer below (each is at most 256 rows: 32 MiB)
 constexpr int kPastEnd = (int)0x80000000u;
 
 template <typename T>
@@ -244,31 +246,44 @@ __global__ __launch_bounds__(256, 1) void i8_stream_shrink_kernel(I8Args g, uint
 
 // ---------------------------------------------------------------------------
 // More than 256 rows.  BM x BN tiles (of w's rows: a gated tile's are BN / 2 of each weight), or pieces of the
-// UNIT_M x UNIT_N ones in the last round.
-template <int BM_, int BN_, int UNIT_M_, int UNIT_N_>
+// UNIT_M x UNIT_N ones in the last round; rings of SX and SW stages.
+//
+// The matrix operations alone (register operands) do 4,700 TOP/s on zeros and 3,650 on random codes, where the chip
+// lowers its clock; in this kernel 4096 x 4096 x 8192 runs at 3,050 on zeros and 2,640 on codes.  16 x 16 x 64
+// operations touch an accumulator half as often as 32 x 32 x 32 ones, and are 7 % faster on codes (5 % slower on
+// zeros).  What a step waits for is the L2: a third stage of one operand, all that the LDS has room for, took 4096 x
+// 4096 x 8192 from 111 to 104 us and the gated 2,961 x 4096 -> 11008 from 230 to 221.
+template <int BM_, int BN_, int SX_, int SW_, int UNIT_M_ = BM_, int UNIT_N_ = BN_>
 struct LongCfg {
-    static constexpr int BM = BM_, BN = BN_, UNIT_M = UNIT_M_, UNIT_N = UNIT_N_;
+    static constexpr int BM = BM_, BN = BN_, SX = SX_, SW = SW_, UNIT_M = UNIT_M_, UNIT_N = UNIT_N_;
 };
-constexpr int kLongWM = 4, kLongWN = 2, kLongWaves = kLongWM * kLongWN, kLongStages = 4;
+constexpr int kLongWM = 4, kLongWN = 2, kLongWaves = kLongWM * kLongWN;
 
 template <class C, int ACT, bool FUSE>
 __global__ __launch_bounds__(kLongWaves * 64, 1) void i8_long_kernel(I8Args g, LoraArgs seg, int tiles_m, int tiles_n, int t0,
                                                                      int count) {
-    constexpr int BM = C::BM, BN = C::BN, WM = kLongWM, WN = kLongWN, NW = kLongWaves, S = kLongStages;
+    constexpr int BM = C::BM, BN = C::BN, SX = C::SX, SW = C::SW, WM = kLongWM, WN = kLongWN, NW = kLongWaves;
     constexpr int SUB_M = C::UNIT_M / BM, SUB_N = C::UNIT_N / BN, SUBS = SUB_M * SUB_N;
     constexpr bool GATED = ACT >= 0;
-    constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
-    constexpr int RB = 64;                                // bytes of a tile row per step
-    constexpr int GX = BM / 16, GW = BN / 16, NL = GX + GW, L = (NL + NW - 1) / NW;   // wave-loads of 16 rows
-    constexpr int SPARE = L * NW == NL ? 0 : 1024;        // where a wave left short loads nothing
-    constexpr int XB = BM * RB, STAGE = (C::UNIT_M + C::UNIT_N) * RB + SPARE;
-    static_assert(SUB_M * BM == C::UNIT_M && SUB_N * BN == C::UNIT_N && WTM % 16 == 0 && WTN % 32 == 0, "tile");
-    static_assert(S * STAGE <= 160 * 1024 && !(GATED && FUSE), "LDS");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds0[STAGE];
-    __shared__ __attribute__((aligned(1024))) uint8_t lds1[STAGE];
-    __shared__ __attribute__((aligned(1024))) uint8_t lds2[STAGE];
-    __shared__ __attribute__((aligned(1024))) uint8_t lds3[STAGE];
-    auto stage = [&](int st) -> uint8_t* { return st == 0 ? lds0 : st == 1 ? lds1 : st == 2 ? lds2 : lds3; };
+    constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;   // blocks of 16 x 16 a wave
+    constexpr int RB = 128;                               // bytes of a tile row per step: a cache line
+    constexpr int LX = BM / 8 / NW, LW = BN / 8 / NW;     // wave-loads of 8 rows a step and wave
+    constexpr int XB = BM * RB, WB = BN * RB;
+    static_assert(SUB_M * BM == C::UNIT_M && SUB_N * BN == C::UNIT_N && FM * 16 == WTM && FN * 16 == WTN && (!GATED || FN % 2 == 0), "tile");
+    static_assert(LX * 8 * NW == BM && LW * 8 * NW == BN && SX * XB + SW * WB <= 160 * 1024 && !(GATED && FUSE), "LDS");
+    static_assert(SX >= 2 && SW >= 2 && SX <= 5 && SW <= 5 && SX - SW <= 1 && SW - SX <= 1, "rings");
+    __shared__ __attribute__((aligned(1024))) uint8_t ldx0[XB];
+    __shared__ __attribute__((aligned(1024))) uint8_t ldx1[XB];
+    __shared__ __attribute__((aligned(1024))) uint8_t ldx2[SX > 2 ? XB : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t ldx3[SX > 3 ? XB : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t ldx4[SX > 4 ? XB : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t ldw0[WB];
+    __shared__ __attribute__((aligned(1024))) uint8_t ldw1[WB];
+    __shared__ __attribute__((aligned(1024))) uint8_t ldw2[SW > 2 ? WB : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t ldw3[SW > 3 ? WB : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t ldw4[SW > 4 ? WB : 16];
+    auto xs_of = [&](int s) -> uint8_t* { return s == 0 ? ldx0 : s == 1 ? ldx1 : s == 2 ? ldx2 : s == 3 ? ldx3 : ldx4; };
+    auto ws_of = [&](int s) -> uint8_t* { return s == 0 ? ldw0 : s == 1 ? ldw1 : s == 2 ? ldw2 : s == 3 ? ldw3 : ldw4; };
     const int M = g.M, N = g.N, K = g.K;
 
     // tiles in groups of 8 rows of tiles, consecutive ones on one XCD: they share slices of x and w in its L2
@@ -285,35 +300,42 @@ __global__ __launch_bounds__(kLongWaves * 64, 1) void i8_long_kernel(I8Args g, L
     const int wm = wave / WN, wn = wave % WN;
     const int li = lane & 15, lg = lane >> 4;
 
-    // this wave's loads: row block b of w's side is rows 16 b .. of the tile; each wave column's WTN of them are
-    // (gated) first WTN / 2 rows of the gate's weight, then as many of the other's, of the same output columns
-    RowBuf buf[L];
-    int at[L];
+    // Rows of a tile's w side: when gated, each wave column's WTN are WTN / 2 of the gate's weight and then as many of the
+    // other's, so that a lane ends with both of an output
+    const RowBuf xb = rows_of(g.x, m0, BM, M, K), wb = rows_of(g.w, n0, ON, N, K);
+    const RowBuf ub = GATED ? rows_of(g.w2, n0, ON, N, K) : wb;
+    // wave-load q of a wave: tile rows 64 q + 8 wave + lane / 8.  Slot p of row r holds chunk p ^ ((r / 2) % 8): reads of
+    // 16 rows are free of bank conflicts
+    const int lr = lane >> 3, chunk = ((lane & 7) ^ ((lr >> 1) | ((wave & 1) << 2))) * 16;
+    const int voff = lr * K + chunk;
+    auto offset = [&](int j) { return j * RB + chunk < K ? voff : kPastEnd; };   // (steps past the end read nothing)
+    auto issue_x = [&](int j, uint8_t* st) {
+        const int off = offset(j);
 #pragma unroll
-    for (int q = 0; q < L; ++q) {
-        const int b = q * NW + wave;
-        if (b < GX) {
-            buf[q] = rows_of(g.x, m0 + 16 * b, 16, M, K);
-        } else if (b < NL) {
-            const int r = 16 * (b - GX), in = r % WTN;
-            const bool up = GATED && in >= WTN / 2;
-            const int col = GATED ? (r / WTN) * (WTN / 2) + (up ? in - WTN / 2 : in) : r;
-            buf[q] = rows_of(up ? g.w2 : g.w, n0 + col, 16, N, K);
-        } else {
-            buf[q] = {uniform(static_cast<const int8_t*>(g.x)), 0};
-        }
-        at[q] = b < NL ? b * 1024 : (C::UNIT_M + C::UNIT_N) * RB;
-    }
-    // lane -> row lane / 4 and slot lane % 4; slot p of row r holds chunk p ^ ((r / 2) % 4): fragment reads
-    // are free of bank conflicts
-    const int chunk = ((lane & 3) ^ ((lane >> 3) & 3)) * 16;
-    const int voff = (lane >> 2) * K + chunk;
-    auto issue = [&](int j, uint8_t* st) {
-        const int kb = j * RB;      // (steps past the end read nothing)
-        const int off = kb + chunk < K ? voff : kPastEnd;
-#pragma unroll
-        for (int q = 0; q < L; ++q) buffer_load_lds16(buf[q].p, buf[q].bytes, st + at[q], off, kb);
+        for (int q = 0; q < LX; ++q)
+            buffer_load_lds16(xb.p, xb.bytes, st + (q * NW + wave) * 1024, off + (64 * q + 8 * wave) * K, j * RB);
     };
+    auto issue_w = [&](int j, uint8_t* st) {
+        const int off = offset(j);
+#pragma unroll
+        for (int q = 0; q < LW; ++q) {
+            const int r = 64 * q + 8 * wave, in = r % WTN;
+            const bool up = GATED && in >= WTN / 2;
+            const int col = GATED ? (r / WTN) * (WTN / 2) + in % (WTN / 2) : r;
+            buffer_load_lds16(up ? ub.p : wb.p, up ? ub.bytes : wb.bytes, st + (q * NW + wave) * 1024,
+                              off + col * K, j * RB);
+        }
+    };
+    // at the end of step j (j >= -max(SX, SW), a constant modulo the rings): what fits into the stages it used.  The
+    // shorter ring goes first: its loads are waited for first.
+    auto refill = [&](int j, int sx, int sw) {
+        if constexpr (SW <= SX) issue_w(j + SW, ws_of(sw));
+        issue_x(j + SX, xs_of(sx));
+        if constexpr (SW > SX) issue_w(j + SW, ws_of(sw));
+    };
+    // loads that may still be on their way when step j + 1's have to be in
+    constexpr int S = SX < SW ? SX : SW;
+    constexpr int OPEN = (S - 2) * (LX + LW) + (SX > SW ? LX : SW > SX ? LW : 0);
 
     // (int32 sums until they are scaled, in place)
     f32x4 acc[FN][FM];
@@ -321,100 +343,145 @@ __global__ __launch_bounds__(kLongWaves * 64, 1) void i8_long_kernel(I8Args g, L
     for (int a = 0; a < FN; ++a)
 #pragma unroll
         for (int b = 0; b < FM; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int foff = (lg ^ ((li >> 1) & 3)) * 16;
-    auto read_frags = [&](const uint8_t* st, u32x4 (&wf)[FN], u32x4 (&xf)[FM]) {
-        const uint8_t* bx = st + (wm * WTM + li) * RB + foff;
-        const uint8_t* bw = st + XB + (wn * WTN + li) * RB + foff;
-#pragma unroll
-        for (int b = 0; b < FM; ++b) xf[b] = *reinterpret_cast<const u32x4*>(bx + b * 16 * RB);
-#pragma unroll
-        for (int a = 0; a < FN; ++a) wf[a] = *reinterpret_cast<const u32x4*>(bw + a * 16 * RB);
-    };
-    auto mma = [&](const u32x4 (&wf)[FN], const u32x4 (&xf)[FM]) {
-#pragma unroll
-        for (int a = 0; a < FN; ++a)
-#pragma unroll
-            for (int b = 0; b < FM; ++b)
-                acc[a][b] = __builtin_bit_cast(f32x4, mma_i8(wf[a], xf[b], __builtin_bit_cast(i32x4, acc[a][b])));
-    };
-    // Fragments of step j + 1 are read while the matrix cores work on step j; step j + S is asked for in step
-    // j's stage once every wave holds step j's fragments.  Whole groups of S steps: those past the end are zeros.
-    u32x4 w0[FN], x0[FM], w1[FN], x1[FM];
-    const int nk = (K + RB * S - 1) / (RB * S) * S;
-#pragma unroll
-    for (int p = 0; p < S; ++p) issue(p, stage(p));
-    wait_vmcnt<(S - 1) * L>();
-    __builtin_amdgcn_s_barrier();
-    read_frags(stage(0), w0, x0);
-    for (int i = 0; i < nk; i += S) {
-#pragma unroll
-        for (int st = 0; st < S; ++st) {
-            __builtin_amdgcn_sched_barrier(0);
-            // this wave's loads of the next step are done, and its fragment reads of this one
-            wait_vmcnt_lgkm0<(S - 2) * L>();
-            // every wave's are
-            __builtin_amdgcn_s_barrier();
-            __builtin_amdgcn_sched_barrier(0);
-            issue(i + st + S, stage(st));
-            if (st % 2 == 0) {
-                read_frags(stage((st + 1) % S), w1, x1);
-                mma(w0, x0);
-            } else {
-                read_frags(stage((st + 1) % S), w0, x0);
-                mma(w1, x1);
-            }
-            // the loads, then each fragment read followed by two matrix operations
-            __builtin_amdgcn_sched_group_barrier(0x020, L, 0);
-#pragma unroll
-            for (int q = 0; q < FN + FM; ++q) {
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
-            }
-        }
-    }
-    wait_vmcnt<0>();   // no load may still be writing LDS
-
-    // lane holds D[n = 4 lg + i][m = li] of each block
-#pragma unroll
-    for (int b = 0; b < FM; ++b) {
-        const int m = m0 + wm * WTM + b * 16 + li;
-        const float xs = m < M ? g.xs[m] : 0.f;
+    // fragments of half h (64 K) of a stage: chunk 4 h + lg of row li of each block
+    const int f0 = (lg ^ ((li >> 1) & 7)) * 16, f1 = f0 ^ 64;
+    const int xrow = (wm * WTM + li) * RB, wrow = (wn * WTN + li) * RB;
+    auto xfrag = [&](const uint8_t* st, int b, int f) { return *reinterpret_cast<const u32x4*>(st + xrow + b * 16 * RB + f); };
+    auto wfrag = [&](const uint8_t* st, int a, int f) { return *reinterpret_cast<const u32x4*>(st + wrow + a * 16 * RB + f); };
+    // One half's matrix operations, with the fragments of the next half read behind them: w's in place as each has
+    // been used, x's into the other set.
+    u32x4 wf[FN], xa[FM], xc[FM];
+    auto half = [&](const uint8_t* sx, const uint8_t* sw, int f, const u32x4 (&x0)[FM], u32x4 (&x1)[FM]) {
 #pragma unroll
         for (int a = 0; a < FN; ++a) {
-            const bool up = GATED && a >= FN / 2;
-            const int n = n0 + (GATED ? wn * (WTN / 2) + (up ? a - FN / 2 : a) * 16 : wn * WTN + a * 16) + 4 * lg;
-            const f32x4 ws = n < N ? *reinterpret_cast<const f32x4*>((up ? g.ws2 : g.ws) + n) : f32x4{0.f, 0.f, 0.f, 0.f};
-            acc[a][b] = scaled(__builtin_bit_cast(i32x4, acc[a][b]), xs, ws);
+#pragma unroll
+            for (int b = 0; b < FM; ++b)
+                acc[a][b] = __builtin_bit_cast(f32x4, mma_i8(wf[a], x0[b], __builtin_bit_cast(i32x4, acc[a][b])));
+            wf[a] = wfrag(sw, a, f);
+            if (a < FM) x1[a] = xfrag(sx, a, f);
         }
+    };
+    constexpr int LPB = (LX + LW + FN - 1) / FN;    // loads between two of w's row blocks
+    auto order = [&](auto loads) {
+        constexpr int LD = decltype(loads)::value;
+#pragma unroll
+        for (int a = 0; a < FM; ++a) {
+            if constexpr (LD > 0) __builtin_amdgcn_sched_group_barrier(0x020, LD, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, FM, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        }
+#pragma unroll
+        for (int a = FM; a < FN; ++a) {
+            if constexpr (LD > 0) __builtin_amdgcn_sched_group_barrier(0x020, LD, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, FM, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // Between the halves every wave holds the stage's last fragments and has the next stage's loads in.
+    auto step = [&](int j, int sx, int sw, int nx, int nw) {
+        half(xs_of(sx), ws_of(sw), f1, xa, xc);
+        order(std::integral_constant<int, 0>{});
+        wait_vmcnt_lgkm0<OPEN>();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        refill(j, sx, sw);
+        half(xs_of(nx), ws_of(nw), f0, xc, xa);
+        order(std::integral_constant<int, LPB>{});
+    };
+    constexpr int U = SX == SW ? SX : SX * SW;     // steps after which both rings are where they were
+    const int nk = (K + RB - 1) / RB;
+    constexpr int S1 = SX > SW ? SX : SW;
+#pragma unroll
+    for (int j = -S1; j < -1; ++j) {
+        if (SW <= SX && j + SW >= 0) issue_w(j + SW, ws_of(j + SW));
+        if (j + SX >= 0) issue_x(j + SX, xs_of(j + SX));
+        if (SW > SX && j + SW >= 0) issue_w(j + SW, ws_of(j + SW));
+    }
+    wait_vmcnt<OPEN>();
+    __builtin_amdgcn_s_barrier();
+    refill(-1, SX - 1, SW - 1);
+#pragma unroll
+    for (int b = 0; b < FM; ++b) xa[b] = xfrag(ldx0, b, f0);
+#pragma unroll
+    for (int a = 0; a < FN; ++a) wf[a] = wfrag(ldw0, a, f0);
+    const int full = nk - nk % U;
+    for (int i = 0; i < full; i += U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) step(i + u, u % SX, u % SW, (u + 1) % SX, (u + 1) % SW);
+    }
+#pragma unroll
+    for (int u = 0; u < U - 1; ++u)
+        if (full + u < nk) step(full + u, u % SX, u % SW, (u + 1) % SX, (u + 1) % SW);
+    wait_vmcnt<0>();   // no load may still be writing LDS
+
+    // lane holds D[n = 4 lg + i][m = li] of each block (rows and columns past the end: the last ones' scales)
+    constexpr int FO = GATED ? FN / 2 : FN, OC = FO * 16;      // output columns of a wave
+    float xs[FM];
+#pragma unroll
+    for (int b = 0; b < FM; ++b) xs[b] = g.xs[min(m0 + wm * WTM + b * 16 + li, M - 1)];
+#pragma unroll
+    for (int a = 0; a < FN; ++a) {
+        const int n = n0 + wn * OC + (a % FO) * 16 + 4 * lg;
+        const f32x4 ws = *reinterpret_cast<const f32x4*>((a >= FO ? g.ws2 : g.ws) + min(n, N - 4));
+#pragma unroll
+        for (int b = 0; b < FM; ++b) acc[a][b] = scaled(__builtin_bit_cast(i32x4, acc[a][b]), xs[b], ws);
     }
     if constexpr (FUSE) {
-        static_assert(C::UNIT_N * kExpandRow * 2 <= STAGE && C::UNIT_M * kExpandRow * 2 <= STAGE, "the expand's operands");
-        expand_segments<BM, BN, WM, WN>(seg, m0, n0, N, reinterpret_cast<uint16_t*>(lds0), reinterpret_cast<uint16_t*>(lds1),
-                                        reinterpret_cast<uint16_t*>(lds2), acc);
+        static_assert(kExpandRow * 2 <= RB, "the expand's operands");
+        expand_segments<BM, BN, WM, WN>(seg, m0, n0, N, reinterpret_cast<uint16_t*>(ldw0), reinterpret_cast<uint16_t*>(ldx0),
+                                        reinterpret_cast<uint16_t*>(ldx1), acc);
     }
+    // The outputs go through LDS, each wave's in a place of its own, so that a store instruction writes whole lines of
+    // rows: straight from the lanes (8 bytes of each of 32 rows) the stores took 18 us of a tile's 70.  Rows whose
+    // delta comes later (decode rows with an adapter) stay unrounded and go straight to ybase.
+    constexpr int CH = OC / 8;      // 16-byte pieces of a wave's rows
+    static_assert(2 * WTM * OC * 2 <= (XB < WB ? XB : WB) && (CH == 16 || CH == 8 || CH == 4 || CH == 2), "outputs");
+    auto raw_row = [&](int m) { return g.row_slot != nullptr && g.row_slot[m] >= 0 && (!FUSE || m >= seg.T_pre); };
+    auto swap_of = [&](int row) { return (row >> (CH == 16 ? 0 : CH == 8 ? 1 : CH == 4 ? 2 : 3)) & (CH - 1); };   // distinct banks
+    uint8_t* mine = ((wave >> 1) == 0 ? ldx0 : (wave >> 1) == 1 ? ldx1 : (wave >> 1) == 2 ? ldw0 : ldw1) + (wave & 1) * (WTM * OC * 2);
+    __syncthreads();   // every wave's loads have landed, and every wave is done with the stages
 #pragma unroll
     for (int b = 0; b < FM; ++b) {
-        const int m = m0 + wm * WTM + b * 16 + li;
-        if (m >= M) continue;
-        // rows whose delta comes later (decode rows with an adapter) stay unrounded
-        const bool raw = g.row_slot != nullptr && g.row_slot[m] >= 0 && (!FUSE || m >= seg.T_pre);
+        const int row = b * 16 + li, m = m0 + wm * WTM + row;
+        const bool raw = !GATED && m < M && raw_row(m);
 #pragma unroll
-        for (int a = 0; a < (GATED ? FN / 2 : FN); ++a) {
-            const int n = n0 + (GATED ? wn * (WTN / 2) : wn * WTN) + a * 16 + 4 * lg;
-            if (n >= N) continue;
-            if constexpr (GATED) put4(g, raw, m, n, gated<ACT>(acc[a][b], acc[a + FN / 2][b]));
-            else put4(g, raw, m, n, acc[a][b]);
+        for (int a = 0; a < FO; ++a) {
+            f32x4 d = acc[a][b];
+            if constexpr (GATED) d = gated<ACT>(d, acc[a + FO][b]);
+            u32x2 o;
+            o[0] = pack_bf16(d[0], d[1]);
+            o[1] = pack_bf16(d[2], d[3]);
+            *reinterpret_cast<u32x2*>(mine + row * (OC * 2) + ((2 * a + (lg >> 1)) ^ swap_of(row)) * 16 + (lg & 1) * 8) = o;
+            const int n = n0 + wn * OC + a * 16 + 4 * lg;
+            if (raw && n < N) *reinterpret_cast<f32x4*>(g.ybase + (int64_t)m * N + n) = d;
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+    const int c8 = lane % CH, n = n0 + wn * OC + c8 * 8;
+#pragma unroll
+    for (int i = 0; i < (WTM * CH + 63) / 64; ++i) {
+        const int row = i * (64 / CH) + lane / CH, m = m0 + wm * WTM + row;
+        if (WTM * CH < 64 && row >= WTM) continue;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(mine + row * (OC * 2) + (c8 ^ swap_of(row)) * 16);
+        if (m >= M || n >= N || (!GATED && raw_row(m))) continue;
+        bf16_t* y = static_cast<bf16_t*>(g.y) + (int64_t)m * N + n;
+        if ((N & 7) == 0) {
+            st16(y, v);
+        } else {      // rows that are 8-byte aligned, and a last piece of four columns
+            *reinterpret_cast<u32x2*>(y) = u32x2{v[0], v[1]};
+            if (n + 4 < N) *reinterpret_cast<u32x2*>(y + 4) = u32x2{v[2], v[3]};
         }
     }
 }
 
-using Long256 = LongCfg<256, 256, 256, 256>;
-using Long256Half = LongCfg<256, 128, 256, 256>;
-using Long256Quarter = LongCfg<128, 128, 256, 256>;
-using Long256Eighth = LongCfg<128, 64, 256, 256>;
-using Long256Sixteenth = LongCfg<64, 64, 256, 256>;
-using Long192 = LongCfg<192, 256, 192, 256>;
-using Long192Half = LongCfg<192, 128, 192, 256>;
+using Long256 = LongCfg<256, 256, 3, 2>;
+using Long256Half = LongCfg<256, 128, 3, 3, 256, 256>;
+using Long256Quarter = LongCfg<128, 128, 4, 4, 256, 256>;
+using Long256Eighth = LongCfg<128, 64, 4, 4, 256, 256>;
+using Long256Sixteenth = LongCfg<64, 64, 5, 5, 256, 256>;
+using Long192 = LongCfg<192, 256, 2, 3>;
+using Long192Half = LongCfg<192, 128, 3, 3, 192, 256>;
 
 template <int ACT, bool FUSE>
 hipError_t run_long(const I8Args& g, const LoraArgs& seg, hipStream_t s) {
