@@ -9,13 +9,13 @@
 // run along K, so a lane's 16 bytes of a row feed one 16 x 16 x 64 step; w is on the operation's M side and x on
 // its N side, and a lane ends with four consecutive output columns of one row.
 //
-//  * i8_stream_kernel (up to 256 rows): bound by reading w once.  A workgroup of four waves holds a tile of
+//  * i8_stream_kernel (tiles of up to 64 x 96): bound by reading w once.  A workgroup of four waves holds a tile of
 //    16 FM rows x 16 FN columns (gated: 8 FN of each weight); wave v takes every fourth slice of 128 K, streams
 //    both operands' rows of its slices through an LDS ring of its own, and holds a whole tile of partial sums.
 //    So no wave waits for another until the end, where the four partial tiles are added in LDS.
-//  * i8_long_kernel (more rows): bound by the matrix operations' power (below).  256 x 256 (or 192 x 256) tiles, eight
-//    waves, steps of 128 K, rings of two and three stages, fragments read half a step ahead; the prefill segments'
-//    expand in the epilogue.
+//  * i8_long_kernel (tiles from 64 x 64 to 256 x 256): long batches are bound by the matrix operations' power (below).
+//    Eight waves, steps of 128 K, rings of two to five stages, fragments read half a step ahead; the prefill
+//    segments' expand in the epilogue.
 //
 // Rows are loaded 128 bytes at a time, whole cache lines: a compute unit has about 512 lines on their way at once, and
 // with 64-byte rows (half a line each) it draws 57 GB/s from the L2 instead of 112.
@@ -88,7 +88,7 @@ __device__ __forceinline__ void put4(const I8Args& g, bool raw, int m, int n, co
 }
 
 // ---------------------------------------------------------------------------
-// Up to 256 rows.  ACT < 0: one weight.
+// Few rows.  ACT < 0: one weight.
 template <int FM_, int FN_, int S_>
 struct StreamCfg {
     static constexpr int FM = FM_, FN = FN_, S = S_;
@@ -245,31 +245,34 @@ __global__ __launch_bounds__(256, 1) void i8_stream_shrink_kernel(I8Args g, uint
 }
 
 // ---------------------------------------------------------------------------
-// More than 256 rows.  BM x BN tiles (of w's rows: a gated tile's are BN / 2 of each weight), or pieces of the
-// UNIT_M x UNIT_N ones in the last round; rings of SX and SW stages.
+// Longer batches.  BM x BN tiles (of w's rows: a gated tile's are BN / 2 of each weight) with rings of SX and SW
+// stages; a launch runs a grid's tiles, or pieces of larger ones.
 //
 // The matrix operations alone (register operands) do 4,700 TOP/s on zeros and 3,650 on random codes, where the chip
 // lowers its clock; in this kernel 4096 x 4096 x 8192 runs at 3,050 on zeros and 2,640 on codes.  16 x 16 x 64
 // operations touch an accumulator half as often as 32 x 32 x 32 ones, and are 7 % faster on codes (5 % slower on
 // zeros).  What a step waits for is the L2: a third stage of one operand, all that the LDS has room for, took 4096 x
 // 4096 x 8192 from 111 to 104 us and the gated 2,961 x 4096 -> 11008 from 230 to 221.
-template <int BM_, int BN_, int SX_, int SW_, int UNIT_M_ = BM_, int UNIT_N_ = BN_>
+template <int BM_, int BN_, int SX_, int SW_>
 struct LongCfg {
-    static constexpr int BM = BM_, BN = BN_, SX = SX_, SW = SW_, UNIT_M = UNIT_M_, UNIT_N = UNIT_N_;
+    static constexpr int BM = BM_, BN = BN_, SX = SX_, SW = SW_;
+};
+// A launch's tiles: t0 .. of a grid of tiles_m x tiles_n tiles of unit_m x unit_n (sub_m, sub_n = 1: a workgroup a
+// tile, count of them; else sub_m x sub_n workgroups a tile).
+struct LongGrid {
+    int tiles_m, tiles_n, t0, count, sub_m, sub_n;
 };
 constexpr int kLongWM = 4, kLongWN = 2, kLongWaves = kLongWM * kLongWN;
 
 template <class C, int ACT, bool FUSE>
-__global__ __launch_bounds__(kLongWaves * 64, 1) void i8_long_kernel(I8Args g, LoraArgs seg, int tiles_m, int tiles_n, int t0,
-                                                                     int count) {
+__global__ __launch_bounds__(kLongWaves * 64, 1) void i8_long_kernel(I8Args g, LoraArgs seg, LongGrid grid) {
     constexpr int BM = C::BM, BN = C::BN, SX = C::SX, SW = C::SW, WM = kLongWM, WN = kLongWN, NW = kLongWaves;
-    constexpr int SUB_M = C::UNIT_M / BM, SUB_N = C::UNIT_N / BN, SUBS = SUB_M * SUB_N;
     constexpr bool GATED = ACT >= 0;
     constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;   // blocks of 16 x 16 a wave
     constexpr int RB = 128;                               // bytes of a tile row per step: a cache line
     constexpr int LX = BM / 8 / NW, LW = BN / 8 / NW;     // wave-loads of 8 rows a step and wave
     constexpr int XB = BM * RB, WB = BN * RB;
-    static_assert(SUB_M * BM == C::UNIT_M && SUB_N * BN == C::UNIT_N && FM * 16 == WTM && FN * 16 == WTN && (!GATED || FN % 2 == 0), "tile");
+    static_assert(FM * 16 == WTM && FN * 16 == WTN && (!GATED || FN % 2 == 0), "tile");
     static_assert(LX * 8 * NW == BM && LW * 8 * NW == BN && SX * XB + SW * WB <= 160 * 1024 && !(GATED && FUSE), "LDS");
     static_assert(SX >= 2 && SW >= 2 && SX <= 5 && SW <= 5 && SX - SW <= 1 && SW - SX <= 1, "rings");
     __shared__ __attribute__((aligned(1024))) uint8_t ldx0[XB];
@@ -287,15 +290,13 @@ __global__ __launch_bounds__(kLongWaves * 64, 1) void i8_long_kernel(I8Args g, L
     const int M = g.M, N = g.N, K = g.K;
 
     // tiles in groups of 8 rows of tiles, consecutive ones on one XCD: they share slices of x and w in its L2
-    const int bid = blockIdx.x;
-    const int t = SUBS > 1 ? t0 + bid / SUBS : t0 + xcd_logical(bid, count);
-    const int group = t / (8 * tiles_n), first_m = group * 8, gm = min(tiles_m - first_m, 8);
-    const int in_group = t - group * 8 * tiles_n;
+    const int bid = blockIdx.x, subs = grid.sub_m * grid.sub_n, piece = bid % subs;
+    const int t = grid.t0 + (subs > 1 ? bid / subs : xcd_logical(bid, grid.count));
+    const int group = t / (8 * grid.tiles_n), first_m = group * 8, gm = min(grid.tiles_m - first_m, 8);
+    const int in_group = t - group * 8 * grid.tiles_n;
     const int tm = first_m + in_group % gm, tn = in_group / gm;
-    const int piece = SUBS > 1 ? bid % SUBS : 0;
-    // output columns of a tile: BN, or of a gated one BN / 2
-    constexpr int ON = GATED ? BN / 2 : BN, UNIT_ON = GATED ? C::UNIT_N / 2 : C::UNIT_N;
-    const int m0 = tm * C::UNIT_M + (piece / SUB_N) * BM, n0 = tn * UNIT_ON + (piece % SUB_N) * ON;
+    constexpr int ON = GATED ? BN / 2 : BN;       // output columns
+    const int m0 = (tm * grid.sub_m + piece / grid.sub_n) * BM, n0 = (tn * grid.sub_n + piece % grid.sub_n) * ON;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int li = lane & 15, lg = lane >> 4;
@@ -475,65 +476,131 @@ __global__ __launch_bounds__(kLongWaves * 64, 1) void i8_long_kernel(I8Args g, L
     }
 }
 
-using Long256 = LongCfg<256, 256, 3, 2>;
-using Long256Half = LongCfg<256, 128, 3, 3, 256, 256>;
-using Long256Quarter = LongCfg<128, 128, 4, 4, 256, 256>;
-using Long256Eighth = LongCfg<128, 64, 4, 4, 256, 256>;
-using Long256Sixteenth = LongCfg<64, 64, 5, 5, 256, 256>;
+// The kinds of tiles.  Up to 64 x 64 the stream's, above it the long ones.
+template <int FM, int FN>
+using Stream = StreamCfg<FM, FN, (FM == 1 && FN == 1) ? 8 : (FM + FN <= 5) ? 4 : (FM + FN == 6) ? 3 : 2>;
+using Long64 = LongCfg<64, 64, 5, 5>;
+using Long128x64 = LongCfg<128, 64, 4, 4>;
+using Long128 = LongCfg<128, 128, 4, 4>;
+using Long192x128 = LongCfg<192, 128, 3, 3>;
+using Long256x128 = LongCfg<256, 128, 3, 3>;
 using Long192 = LongCfg<192, 256, 2, 3>;
-using Long192Half = LongCfg<192, 128, 3, 3, 192, 256>;
+using Long256 = LongCfg<256, 256, 3, 2>;
+
+struct Kind {
+    int bm, bn;     // rows of x and of the weights
+    bool stream;
+};
+constexpr Kind kKinds[] = {
+    {16, 16, true}, {16, 32, true}, {16, 48, true}, {16, 64, true}, {16, 96, true},
+    {32, 16, true}, {32, 32, true}, {32, 48, true}, {32, 64, true}, {32, 96, true},
+    {64, 16, true}, {64, 32, true}, {64, 48, true}, {64, 64, true}, {64, 96, true},
+    {64, 64, false}, {128, 64, false}, {128, 128, false}, {192, 128, false}, {256, 128, false}, {192, 256, false}, {256, 256, false}};
+
+int64_t tiles_of(const I8Args& g, const Kind& k, bool two) {
+    return (int64_t)((g.M + k.bm - 1) / k.bm) * (((int64_t)g.N * (two ? 2 : 1) + k.bn - 1) / k.bn);
+}
+
+// us of a round of tiles, one a compute unit: a step of 128 K waits for its lines (2.06 ns a row: all that a compute
+// unit draws) or for the matrix operations (2.2e-5 us an output with every compute unit at work); fill and
+// epilogue.  Measured against it (cold weights, us): 64 x 4096 x 4096 in 32 x 32 tiles 8.5, 64 x 64 13.3; 64 -> 11008 in
+// 64 x 48 14.6, 32 x 48 18.9; 256 x 4096 x 4096 in 64 x 64 11.8, 128 x 64 15.4, 128 x 128 20.5; 256 -> 11008 in 128 x 128
+// 23.6, 64 x 64 29.6, 256 x 128 32.0; gated 256 -> 11008 in 256 x 128 36.2, 128 x 128 46.7, 64 x 96 55.9.
+double round_us(const Kind& k, int K) {
+    const double lines = 2.06e-3 * (k.bm + k.bn), ops = 2.2e-5 * k.bm * k.bn;
+    return 1.0 + (K / 128.0) * (lines > ops ? lines : ops);
+}
+
+// How a product is run: one kind of tile, or whole 256-column tiles with their partial last round cut into pieces.
+struct Choice {
+    Kind kind;
+    int rem, sub_m, sub_n;      // tiles of the last round in pieces, and pieces a tile
+};
+
+// seg: only long tiles add the segments' expand themselves
+Choice choose(const I8Args& g, bool two, bool seg) {
+    const int cus = gemm_cu_count();
+    Choice best{};
+    double us = 1e30;
+    for (const Kind& k : kKinds) {
+        if (k.stream ? seg || g.M > 256 || (two && k.bn % 32 != 0) : g.M <= 64 && !seg) continue;
+        // rows of x beside those that exist would only be read past
+        if (k.stream && k.bm >= 32 && g.M <= k.bm / 2) continue;
+        const int64_t tiles = tiles_of(g, k, two);
+        const double one = round_us(k, g.K);
+        double t = one * (double)((tiles + cus - 1) / cus);
+        // the stream's tiles of 64 x 64 are the better ones of this size from K = 8192 on (256 x 4096: 26.4 us against 27.9 at
+        // K = 11008, 12.8 against 11.8 at 4096)
+        if (k.bm == 64 && k.bn == 64 && k.stream == (g.K < 8192)) t += 0.01;
+        if (t < us) {
+            us = t;
+            best = {k, 0, 1, 1};
+        }
+        if (k.stream || k.bn != 256 || tiles <= cus || tiles > INT32_MAX) continue;
+        // the last round in pieces, as many a tile as the chip holds at once (halves may take two rounds)
+        const int rem = (int)(tiles % cus);
+        if (rem == 0) continue;
+        const bool tall = k.bm == 256;
+        Choice c{k, rem, 1, 2};
+        if (tall && rem * 16 <= cus) c = {k, rem, 4, 4};
+        else if (tall && rem * 8 <= cus) c = {k, rem, 2, 4};
+        else if (tall && rem * 4 <= cus) c = {k, rem, 2, 2};
+        const int pieces = c.sub_m * c.sub_n;
+        const double more = 2.0 + round_us({k.bm / c.sub_m, k.bn / c.sub_n, false}, g.K) * ((rem * pieces + cus - 1) / cus);
+        t = one * (double)(tiles / cus) + more;
+        if (t < us) {
+            us = t;
+            best = c;
+        }
+    }
+    return best;
+}
 
 template <int ACT, bool FUSE>
-hipError_t run_long(const I8Args& g, const LoraArgs& seg, hipStream_t s) {
-    // Tile height 256 or 192 by the estimated time of its rounds (one workgroup a compute unit), as for the
-    // bf16 base; the partial last round runs as pieces of tiles.
-    const int cus = gemm_cu_count(), on = ACT >= 0 ? 128 : 256;
-    auto pieces = [&](int rem) { return rem * 16 <= cus ? 16 : rem * 8 <= cus ? 8 : rem * 4 <= cus ? 4 : 2; };
-    auto plan = [&](int bm, int& tm, int& tn, int& rem) {
-        tm = (g.M + bm - 1) / bm;
-        tn = (g.N + on - 1) / on;
-        const int tiles = tm * tn;
-        rem = tiles > cus ? tiles % cus : 0;
-        const double f = bm == 256 ? 1.0 : 0.85;
-        if (tiles <= cus) return f * (1.0 - 0.58 * (1.0 - (double)tiles / cus));
-        double tail = 0.0;
-        if (rem) {
-            const int p = bm == 256 ? pieces(rem) : 2;
-            tail = p == 2 ? (bm == 256 ? 0.5 : 0.58) * ((2 * rem + cus - 1) / cus) : 1.5 / p;
-        }
-        return f * (tiles / cus + tail);
+hipError_t run_long(const I8Args& g, const LoraArgs& seg, const Choice& c, hipStream_t s) {
+    const int bn = ACT >= 0 ? c.kind.bn / 2 : c.kind.bn;
+    const int tm = (g.M + c.kind.bm - 1) / c.kind.bm, tn = (g.N + bn - 1) / bn, whole = tm * tn - c.rem;
+    auto go = [&](int bm, int bn, const LongGrid& grid, int blocks) {
+        auto run = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(blocks), dim3(kLongWaves * 64), 0, s, g, seg, grid); };
+        if (bm == 64) run(i8_long_kernel<Long64, ACT, FUSE>);
+        else if (bm == 128 && bn == 64) run(i8_long_kernel<Long128x64, ACT, FUSE>);
+        else if (bm == 128) run(i8_long_kernel<Long128, ACT, FUSE>);
+        else if (bm == 192 && bn == 128) run(i8_long_kernel<Long192x128, ACT, FUSE>);
+        else if (bn == 128) run(i8_long_kernel<Long256x128, ACT, FUSE>);
+        else if (bm == 192) run(i8_long_kernel<Long192, ACT, FUSE>);
+        else run(i8_long_kernel<Long256, ACT, FUSE>);
     };
-    int tm, tn, rem, tm2, tn2, rem2;
-    const bool tall = plan(256, tm, tn, rem) <= plan(192, tm2, tn2, rem2);
-    if (!tall) {
-        tm = tm2;
-        tn = tn2;
-        rem = rem2;
-    }
-    const int n_main = tm * tn - rem, np = tall && rem ? pieces(rem) : 2;
-    auto go = [&](auto whole, auto piece) {
-        hipLaunchKernelGGL(whole, dim3(n_main), dim3(kLongWaves * 64), 0, s, g, seg, tm, tn, 0, n_main);
-        if (rem) hipLaunchKernelGGL(piece, dim3(np * rem), dim3(kLongWaves * 64), 0, s, g, seg, tm, tn, n_main, rem);
-    };
-    if (!tall) go(i8_long_kernel<Long192, ACT, FUSE>, i8_long_kernel<Long192Half, ACT, FUSE>);
-    else if (np == 16) go(i8_long_kernel<Long256, ACT, FUSE>, i8_long_kernel<Long256Sixteenth, ACT, FUSE>);
-    else if (np == 8) go(i8_long_kernel<Long256, ACT, FUSE>, i8_long_kernel<Long256Eighth, ACT, FUSE>);
-    else if (np == 4) go(i8_long_kernel<Long256, ACT, FUSE>, i8_long_kernel<Long256Quarter, ACT, FUSE>);
-    else go(i8_long_kernel<Long256, ACT, FUSE>, i8_long_kernel<Long256Half, ACT, FUSE>);
+    if (whole > 0) go(c.kind.bm, c.kind.bn, LongGrid{tm, tn, 0, whole, 1, 1}, whole);
+    if (c.rem > 0)
+        go(c.kind.bm / c.sub_m, c.kind.bn / c.sub_n, LongGrid{tm, tn, whole, c.rem, c.sub_m, c.sub_n}, c.rem * c.sub_m * c.sub_n);
     return hipGetLastError();
 }
 
-// Stream tiles: rows in blocks of 16, 32 or 64, and the fewest columns that leave at most a tile a compute
-// unit (w then streams through all of them in one round, and x is read as seldom as that allows).
-template <class Go>
-void stream_shape(const I8Args& g, bool two, Go go) {
-    const int cus = gemm_cu_count();
-    const int fm = g.M <= 16 ? 1 : g.M <= 32 ? 2 : 4;
-    const int rb = (g.M + 16 * fm - 1) / (16 * fm);
-    const int blocks = (g.N + 15) / 16 * (two ? 2 : 1);   // 16-row blocks of the weights
-    int fn = two ? 2 : 1;
-    while (fn < 4 && (int64_t)rb * ((blocks + fn - 1) / fn) > cus) fn += two ? 2 : 1;
-    go(fm, fn, (unsigned)(rb * ((blocks + fn - 1) / fn)));
+// go(kernel tile's configuration) for a stream tile of bm x bn
+template <bool TWO, class Go>
+void with_stream(const Kind& k, Go go) {
+    auto by_rows = [&](auto fnc) {
+        constexpr int FN = decltype(fnc)::value;
+        if (k.bm == 16) go(Stream<1, FN>{});
+        else if (k.bm == 32) go(Stream<2, FN>{});
+        else go(Stream<4, FN>{});
+    };
+    if (k.bn == 32) by_rows(std::integral_constant<int, 2>{});
+    else if (k.bn == 64) by_rows(std::integral_constant<int, 4>{});
+    else if (k.bn == 96) by_rows(std::integral_constant<int, 6>{});
+    else if constexpr (!TWO) {
+        if (k.bn == 16) by_rows(std::integral_constant<int, 1>{});
+        else by_rows(std::integral_constant<int, 3>{});
+    }
+}
+
+template <int ACT>
+hipError_t run_stream(const I8Args& g, const Kind& k, hipStream_t s) {
+    const unsigned tiles = (unsigned)tiles_of(g, k, ACT >= 0);
+    with_stream<(ACT >= 0)>(k, [&](auto c) {
+        hipLaunchKernelGGL((i8_stream_kernel<decltype(c), ACT>), dim3(tiles), dim3(256), 0, s, g);
+    });
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -542,49 +609,23 @@ bool gemm_i8_ok(int64_t M, int64_t N, int64_t K) {
     return M >= 1 && M <= kI8MaxRows && N >= 4 && N <= kI8MaxRows && N % 4 == 0 && K >= 16 && K <= kI8MaxK && K % 16 == 0;
 }
 
-namespace {
-
-template <int FM, int FN>
-using Stream = StreamCfg<FM, FN, (FM == 1 && FN == 1) ? 8 : (FM + FN <= 5) ? 4 : (FM + FN == 6 && FM == 4) ? 3 : 2>;
-
-template <int ACT>
-hipError_t run_stream(const I8Args& g, hipStream_t s) {
-    stream_shape(g, ACT >= 0, [&](int fm, int fn, unsigned grid) {
-        auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(grid), dim3(256), 0, s, g); };
-        auto by_fm = [&](auto fnc) {
-            constexpr int FN = decltype(fnc)::value;
-            if (fm == 1) go(i8_stream_kernel<Stream<1, FN>, ACT>);
-            else if (fm == 2) go(i8_stream_kernel<Stream<2, FN>, ACT>);
-            else go(i8_stream_kernel<Stream<4, FN>, ACT>);
-        };
-        if (fn == 2) by_fm(std::integral_constant<int, 2>{});
-        else if (fn >= 4) by_fm(std::integral_constant<int, 4>{});
-        else if constexpr (ACT < 0) {
-            if (fn == 1) by_fm(std::integral_constant<int, 1>{});
-            else by_fm(std::integral_constant<int, 3>{});
-        }
-    });
-    return hipGetLastError();
-}
-
-}  // namespace
-
 hipError_t launch_gemm_i8(const I8Args& g, const LoraArgs* seg, bool* fused, hipStream_t s) {
     if (fused) *fused = false;
     if (!gemm_i8_ok(g.M, g.N, g.K)) return hipErrorInvalidValue;
-    if (g.M <= 256) return run_stream<-1>(g, s);
-    if (seg != nullptr && seg->n_segs > 0) {
-        if (fused) *fused = true;
-        return run_long<-1, true>(g, *seg, s);
-    }
-    return run_long<-1, false>(g, LoraArgs{}, s);
+    const bool fuse = fused != nullptr && seg != nullptr && seg->n_segs > 0;
+    const Choice c = choose(g, false, fuse);
+    if (c.kind.stream) return run_stream<-1>(g, c.kind, s);
+    if (!fuse) return run_long<-1, false>(g, LoraArgs{}, c, s);
+    *fused = true;
+    return run_long<-1, true>(g, *seg, c, s);
 }
 
 hipError_t launch_gemm_i8_gated(const I8Args& g, int act, hipStream_t s) {
     if (!gemm_i8_ok(g.M, g.N, g.K) || g.row_slot != nullptr) return hipErrorInvalidValue;
+    const Choice c = choose(g, true, false);
     auto go = [&](auto actc) {
         constexpr int ACT = decltype(actc)::value;
-        return g.M <= 256 ? run_stream<ACT>(g, s) : run_long<ACT, false>(g, LoraArgs{}, s);
+        return c.kind.stream ? run_stream<ACT>(g, c.kind, s) : run_long<ACT, false>(g, LoraArgs{}, c, s);
     };
     switch (act) {
         case kActSilu: return go(std::integral_constant<int, kActSilu>{});
@@ -602,22 +643,26 @@ hipError_t launch_gemm_i8_shrink(const I8Args& g0, uint64_t raw_mask, const Lora
     I8Args g = g0;
     if (raw_mask != 0) g.row_slot = nullptr;
     const int ncp = cp_n > 0 ? kCopyBlocks : 0;
-    stream_shape(g, false, [&](int fm, int fn, unsigned tiles) {
-        auto go = [&](auto kern) {
-            hipLaunchKernelGGL(kern, dim3(tiles + a.n_su + ncp), dim3(256), 0, s, g, raw_mask, a, (int)tiles,
-                               static_cast<const uint32_t*>(cp_src), static_cast<uint32_t*>(cp_dst), (int)cp_n);
-        };
-        auto by_fm = [&](auto fnc) {
-            constexpr int FN = decltype(fnc)::value;
-            if (fm == 1) go(i8_stream_shrink_kernel<Stream<1, FN>>);
-            else if (fm == 2) go(i8_stream_shrink_kernel<Stream<2, FN>>);
-            else go(i8_stream_shrink_kernel<Stream<4, FN>>);
-        };
-        if (fn == 1) by_fm(std::integral_constant<int, 1>{});
-        else if (fn == 2) by_fm(std::integral_constant<int, 2>{});
-        else if (fn == 3) by_fm(std::integral_constant<int, 3>{});
-        else by_fm(std::integral_constant<int, 4>{});
-    });
+    const int cus = gemm_cu_count();
+    // Tiles that leave room for a second workgroup in a compute unit, so that the shrink's units run beside them and
+    // not behind; the rows and columns that read least where every tile has a compute unit of its own.
+    auto go = [&](auto cfg) {
+        using C = decltype(cfg);
+        const unsigned tiles = (unsigned)tiles_of(g, Kind{16 * C::FM, 16 * C::FN, true}, false);
+        hipLaunchKernelGGL((i8_stream_shrink_kernel<C>), dim3(tiles + a.n_su + ncp), dim3(256), 0, s, g, raw_mask, a, (int)tiles,
+                           static_cast<const uint32_t*>(cp_src), static_cast<uint32_t*>(cp_dst), (int)cp_n);
+    };
+    const int blocks = (g.N + 15) / 16;
+    if (g.M <= 16) {
+        if (blocks <= cus) go(StreamCfg<1, 1, 4>{});
+        else go(StreamCfg<1, 3, 2>{});
+    } else if (g.M <= 32) {
+        if (blocks <= cus) go(StreamCfg<2, 1, 3>{});
+        else go(StreamCfg<2, 3, 2>{});
+    } else {
+        if (blocks <= cus) go(StreamCfg<2, 2, 2>{});
+        else go(StreamCfg<4, 3, 2>{});
+    }
     return hipGetLastError();
 }
 

@@ -100,11 +100,18 @@ __device__ __forceinline__ void put_form(const RowsArgs& a, int64_t row, int v, 
     }
 }
 
+// the row of this wave or workgroup (the grid has a second dimension where its threads would pass 32 bits)
+template <bool WAVE>
+__device__ __forceinline__ int64_t row_here() {
+    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    return WAVE ? block * 4 + (threadIdx.x >> 6) : block;
+}
+
 // NV vectors of 8 values a thread; WAVE: a wave a row and four rows a workgroup, else a workgroup a row
 template <int NV, bool WAVE>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void rows_norm_kernel(RowsArgs a) {
-    const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-    if (WAVE && row >= a.n_rows) return;
+    const int64_t row = row_here<WAVE>();
+    if (row >= a.n_rows) return;
     const int t = WAVE ? threadIdx.x & 63 : threadIdx.x, nt = WAVE ? 64 : blockDim.x, vecs = a.d >> 3;
     const u32x4 none = {0u, 0u, 0u, 0u};
     u32x4 h[NV], w[NV];
@@ -174,8 +181,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rows_norm_kernel(RowsArgs a
 
 template <int NV, bool WAVE, int ACT>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void rows_act_kernel(RowsArgs a) {
-    const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-    if (WAVE && row >= a.n_rows) return;
+    const int64_t row = row_here<WAVE>();
+    if (row >= a.n_rows) return;
     const int t = WAVE ? threadIdx.x & 63 : threadIdx.x, nt = WAVE ? 64 : blockDim.x, vecs = a.d >> 3;
     const u32x4 none = {0u, 0u, 0u, 0u};
     u32x4 h[NV], gv[NV];
@@ -232,7 +239,11 @@ hipError_t by_width(const RowsArgs& a, Go go) {
     if (a.n_rows < 1 || a.d < 8 || a.d % 8 || a.d > kMaxRowWidth) return hipErrorInvalidValue;
     const int vecs = a.d / 8;
     auto waves = [&](int nv) { return dim3((vecs + nv * 64 - 1) / (nv * 64) * 64); };
-    const dim3 rows(a.n_rows), fours((a.n_rows + 3) / 4), four(256);
+    auto grid = [](int64_t blocks) {
+        constexpr int64_t kMost = 1 << 20;
+        return blocks <= kMost ? dim3((unsigned)blocks) : dim3((unsigned)kMost, (unsigned)((blocks + kMost - 1) / kMost));
+    };
+    const dim3 rows = grid(a.n_rows), fours = grid(((int64_t)a.n_rows + 3) / 4), four(256);
     if (vecs <= 64) go.template operator()<1, true>(fours, four);
     else if (vecs <= 128) go.template operator()<2, true>(fours, four);
     else if (vecs <= 512) go.template operator()<1, false>(rows, waves(1));
