@@ -235,6 +235,19 @@ def current_stream(device: int) -> int:
     return _raw_stream(device)
 
 
+_raw_device = None
+
+
+def _current_device() -> int:
+    """The current GPU (torch's own raw accessor where it has one, once torch.cuda is initialised)."""
+    global _raw_device
+    if _raw_device is None:
+        import torch
+        torch.cuda.init()
+        _raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _raw_device()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
@@ -259,14 +272,13 @@ def _on_gpu(stream, call, *tensors) -> None:
     if dev is None:
         call(_stream(stream))
         return
-    import torch
-    if stream is None:
-        stream = current_stream(dev)
-    if torch.cuda.current_device() == dev:
-        call(_stream(stream))
+    stream = current_stream(dev) if stream is None else _stream(stream)
+    if _current_device() == dev:
+        call(stream)
     else:
+        import torch
         with torch.cuda.device(dev):
-            call(_stream(stream))
+            call(stream)
 
 
 class Pool:
@@ -526,84 +538,93 @@ def lora_linear_w4(pool: Pool, plan: Plan, layer: int, proj: int, x, w0_code, w0
                                       "lora_linear_w4"), pool.pages, x, w0_code, w0_scale, y)
 
 
-_row_types = None
-
-
-def _rows(name: str, t, n: int, d: int, device: int):
-    """Address and row stride of bf16 rows [n, d] on a GPU (None: NULL)."""
-    if t is None:
-        return None, 0
-    shape, st = t.shape, t.stride()
-    if t.dtype is not _row_types[0] or t.get_device() != device or len(shape) != 2 or shape[0] != n or shape[1] != d or st[1] != 1:
-        raise ValueError(f"{name}: bfloat16 rows [{n}, {d}], contiguous along a row, on the GPU of x are needed")
-    return t.data_ptr(), st[0] if n > 1 else d
-
-
-def _form(code, scale, n: int, d: int, device: int):
-    """Addresses of the codes [n, d] and scales [n] of rows (both None: NULL)."""
-    if code is None and scale is None:
-        return None, None
-    if code is None or scale is None or code.dtype is not _row_types[1] or scale.dtype is not _row_types[2] or \
-            code.get_device() != device or scale.get_device() != device or tuple(code.shape) != (n, d) or \
-            tuple(scale.shape) != (n,) or not code.is_contiguous() or not scale.is_contiguous():
-        raise ValueError(f"code and scale: contiguous int8 [{n}, {d}] and float32 [{n}] on the GPU of x, together")
-    return code.data_ptr(), scale.data_ptr()
-
-
-def _rows_call(name: str, x, stream, rows) -> None:
-    import torch
-    dev = x.get_device()
-    if dev < 0:
-        raise ValueError(f"{name}: x must be on a GPU")
-    st = current_stream(dev) if stream is None else _stream(stream)
-    if torch.cuda.current_device() == dev:
-        _check(getattr(library(), name)(rows, st), name)
-    else:
-        with torch.cuda.device(dev):
-            _check(getattr(library(), name)(rows, st), name)
+_BF16 = _INT8 = _FP32 = None
 
 
 def _row_shape(x):
-    global _row_types
-    if _row_types is None:
+    """Shape of bf16 rows and the GPU that holds them."""
+    global _BF16, _INT8, _FP32
+    if _BF16 is None:
         import torch
-        _row_types = torch.bfloat16, torch.int8, torch.float32
-    if x.dim() != 2:
-        raise ValueError(f"x: rows [n, d] are needed, not {tuple(x.shape)}")
-    return x.shape[0], x.shape[1], x.get_device()
+        _BF16, _INT8, _FP32 = torch.bfloat16, torch.int8, torch.float32
+    shape, dev = x.shape, x.get_device()
+    if len(shape) != 2:
+        raise ValueError(f"x: rows [n, d] are needed, not {tuple(shape)}")
+    return shape, dev
+
+
+def _rows(name: str, t, shape, dev: int):
+    """Address and row stride of bf16 rows of a shape on a GPU (None: NULL)."""
+    if t is None:
+        return None, 0
+    row, one = t.stride() if t.dim() == 2 else (0, 0)
+    if one != 1 or t.shape != shape or t.dtype is not _BF16 or t.get_device() != dev:
+        raise ValueError(f"{name}: bfloat16 rows {list(shape)}, contiguous along a row, on the GPU of x are needed")
+    return t.data_ptr(), row
+
+
+def _form(code, scale, shape, dev: int):
+    """Addresses of the codes [n, d] and scales [n] of rows (both None: NULL)."""
+    if code is None and scale is None:
+        return None, None
+    if code is None or scale is None or code.shape != shape or code.dtype is not _INT8 or scale.dtype is not _FP32 or \
+            scale.dim() != 1 or scale.shape[0] != shape[0] or code.get_device() != dev or scale.get_device() != dev or \
+            not code.is_contiguous() or not scale.is_contiguous():
+        raise ValueError(f"code and scale: contiguous int8 {list(shape)} and float32 [{shape[0]}] on the GPU of x, together")
+    return code.data_ptr(), scale.data_ptr()
+
+
+def _rows_call(name: str, rows, dev: int, stream) -> None:
+    if dev < 0:
+        raise ValueError(f"{name}: x must be on a GPU")
+    call = getattr(library(), name)
+    stream = current_stream(dev) if stream is None else _stream(stream)
+    if _current_device() == dev:
+        rc = call(rows, stream)
+    else:
+        import torch
+        with torch.cuda.device(dev):
+            rc = call(rows, stream)
+    if rc != LORA_OK:
+        _check(rc, name)
 
 
 def rows_norm_i8(x, weight, eps: float, residual=None, sum_out=None, y=None, code=None, scale=None, held=None,
                  stream=None) -> None:
     """Norm of bf16 rows x (+ residual) [n, d] with the weight [d]: y, and the 8-bit form code, scale, held."""
-    n, d, dev = _row_shape(x)
-    if weight.dtype is not _row_types[0] or tuple(weight.shape) != (d,) or weight.get_device() != dev or \
+    shape, dev = _row_shape(x)
+    if weight.dtype is not _BF16 or weight.dim() != 1 or weight.shape[0] != shape[1] or weight.get_device() != dev or \
             not weight.is_contiguous():
-        raise ValueError(f"weight: contiguous bfloat16 [{d}] on the GPU of x is needed")
-    xp, xs = _rows("x", x, n, d, dev)
-    rp, rs = _rows("residual", residual, n, d, dev)
-    sp, ss = _rows("sum_out", sum_out, n, d, dev)
-    yp, ys = _rows("y", y, n, d, dev)
-    hp, hs = _rows("held", held, n, d, dev)
-    cp, fp = _form(code, scale, n, d, dev)
-    _rows_call("rows_norm_i8", x, stream, lora_norm_rows(n, d, eps, xp, rp, weight.data_ptr(), sp, yp, hp, cp, fp, xs, rs,
-                                                         ss, ys, hs))
+        raise ValueError(f"weight: contiguous bfloat16 [{shape[1]}] on the GPU of x is needed")
+    xp, xs = _rows("x", x, shape, dev)
+    rp, rs = _rows("residual", residual, shape, dev)
+    sp, ss = _rows("sum_out", sum_out, shape, dev)
+    yp, ys = _rows("y", y, shape, dev)
+    hp, hs = _rows("held", held, shape, dev)
+    cp, fp = _form(code, scale, shape, dev)
+    _rows_call("rows_norm_i8", lora_norm_rows(shape[0], shape[1], eps, xp, rp, weight.data_ptr(), sp, yp, hp, cp, fp, xs, rs,
+                                              ss, ys, hs), dev, stream)
+
+
+def _act(act) -> int:
+    if isinstance(act, str):
+        if act not in ACTS:
+            raise ValueError(f"act {act!r}: one of {', '.join(ACTS)}")
+        act = ACTS[act]
+    return act
 
 
 def rows_act_i8(x, gate=None, act="none", y=None, code=None, scale=None, held=None, stream=None) -> None:
     """a = act(gate) * x (x alone with "none") of bf16 rows [n, d]: y, and its 8-bit form code, scale, held.
     act: "none", "silu", "gelu", "gelu_tanh" or a LORA_ACT_* number."""
-    n, d, dev = _row_shape(x)
-    if isinstance(act, str):
-        if act not in ACTS:
-            raise ValueError(f"act {act!r}: one of {', '.join(ACTS)}")
-        act = ACTS[act]
-    xp, xs = _rows("x", x, n, d, dev)
-    gp, gs = _rows("gate", gate, n, d, dev)
-    yp, ys = _rows("y", y, n, d, dev)
-    hp, hs = _rows("held", held, n, d, dev)
-    cp, fp = _form(code, scale, n, d, dev)
-    _rows_call("rows_act_i8", x, stream, lora_act_rows(n, d, act, xp, gp, yp, hp, cp, fp, xs, gs, ys, hs))
+    act = _act(act)
+    shape, dev = _row_shape(x)
+    xp, xs = _rows("x", x, shape, dev)
+    gp, gs = _rows("gate", gate, shape, dev)
+    yp, ys = _rows("y", y, shape, dev)
+    hp, hs = _rows("held", held, shape, dev)
+    cp, fp = _form(code, scale, shape, dev)
+    _rows_call("rows_act_i8", lora_act_rows(shape[0], shape[1], act, xp, gp, yp, hp, cp, fp, xs, gs, ys, hs), dev, stream)
 
 
 def base_gemm_i8(x_code, x_scale, w0_code, w0_scale, y, M: int, N: int, K: int, stream=None) -> None:
@@ -615,10 +636,7 @@ def base_gemm_i8(x_code, x_scale, w0_code, w0_scale, y, M: int, N: int, K: int, 
 def base_gated_i8(x_code, x_scale, wg_code, wg_scale, wu_code, wu_scale, y, M: int, N: int, K: int, act="silu",
                   stream=None) -> None:
     """y = act(gate) * up of one feed-forward block; act: "silu", "gelu", "gelu_tanh" or a LORA_ACT_* number."""
-    if isinstance(act, str):
-        if act not in ACTS:
-            raise ValueError(f"act {act!r}: one of {', '.join(ACTS)}")
-        act = ACTS[act]
+    act = _act(act)
     _on_gpu(stream, lambda st: _check(library().base_gated_i8(_addr(x_code), _addr(x_scale), _addr(wg_code), _addr(wg_scale),
                                                               _addr(wu_code), _addr(wu_scale), act, _addr(y), M, N, K, st),
                                       "base_gated_i8"), x_code, x_scale, wg_code, wg_scale, wu_code, wu_scale, y)

@@ -18,8 +18,9 @@ int check_row_sizes(int64_t n_rows, int32_t d) {
     return LORA_OK;
 }
 
-// bf16 rows: 16-byte aligned, a stride that keeps them so and apart
-int check_rows(const char* name, const void* p, int64_t stride, int32_t d) {
+// bf16 rows: 16-byte aligned, a stride that keeps them so and apart (one row's says nothing)
+int check_rows(const char* name, const void* p, int64_t n, int64_t stride, int32_t d) {
+    if (n == 1) stride = d;
     if ((uintptr_t)p % 16 || stride % 8) return set_error(LORA_EINVAL, "%s: 16-byte aligned rows (stride a multiple of 8)", name);
     if (stride < d || stride > (int64_t(1) << 32)) return set_error(LORA_EINVAL, "%s: row stride %lld of rows of %d", name, (long long)stride, d);
     return LORA_OK;
@@ -70,11 +71,11 @@ int rows_norm_i8(const lora_norm_rows* r, void* stream) {
     if (!r->x || !r->weight) return set_error(LORA_EINVAL, "x or weight is NULL");
     if ((uintptr_t)r->weight % 16) return set_error(LORA_EINVAL, "weight must be 16-byte aligned");
     if (r->sum_out && !r->residual) return set_error(LORA_EINVAL, "sum_out without a residual");
-    CHECK(check_rows("x", r->x, r->x_stride, r->d));
-    if (r->residual) CHECK(check_rows("residual", r->residual, r->residual_stride, r->d));
-    if (r->sum_out) CHECK(check_rows("sum_out", r->sum_out, r->sum_stride, r->d));
-    if (r->y) CHECK(check_rows("y", r->y, r->y_stride, r->d));
-    if (r->held) CHECK(check_rows("held", r->held, r->held_stride, r->d));
+    CHECK(check_rows("x", r->x, r->n_rows, r->x_stride, r->d));
+    if (r->residual) CHECK(check_rows("residual", r->residual, r->n_rows, r->residual_stride, r->d));
+    if (r->sum_out) CHECK(check_rows("sum_out", r->sum_out, r->n_rows, r->sum_stride, r->d));
+    if (r->y) CHECK(check_rows("y", r->y, r->n_rows, r->y_stride, r->d));
+    if (r->held) CHECK(check_rows("held", r->held, r->n_rows, r->held_stride, r->d));
     CHECK(check_form(r->y, r->held, r->code, r->scale));
     RowsArgs a{};
     a.x = r->x;
@@ -104,10 +105,10 @@ int rows_act_i8(const lora_act_rows* r, void* stream) {
         return set_error(LORA_EINVAL, "a gate goes with an activation, and none without");
     if (r->n_rows == 0) return LORA_OK;
     if (!r->x) return set_error(LORA_EINVAL, "x is NULL");
-    CHECK(check_rows("x", r->x, r->x_stride, r->d));
-    if (r->gate) CHECK(check_rows("gate", r->gate, r->gate_stride, r->d));
-    if (r->y) CHECK(check_rows("y", r->y, r->y_stride, r->d));
-    if (r->held) CHECK(check_rows("held", r->held, r->held_stride, r->d));
+    CHECK(check_rows("x", r->x, r->n_rows, r->x_stride, r->d));
+    if (r->gate) CHECK(check_rows("gate", r->gate, r->n_rows, r->gate_stride, r->d));
+    if (r->y) CHECK(check_rows("y", r->y, r->n_rows, r->y_stride, r->d));
+    if (r->held) CHECK(check_rows("held", r->held, r->n_rows, r->held_stride, r->d));
     CHECK(check_form(r->y, r->held, r->code, r->scale));
     RowsArgs a{};
     a.x = r->x;
