@@ -2,9 +2,10 @@
 //
 // A row p of d values has the 8-bit form scale * code: m = max |p|, code_j the integer nearest to
 // 127 p_j / m (ties to even), scale = m / 127 (the norm: m r / 127).  The codes are exact: with p and m
-// scaled by the power of two that brings m to [1, 2), 127 p has at most 23 significant bits (p is a
-// product of two bf16 numbers, or one), a candidate q from a product with 127 / m is at most one off,
-// and e = 127 p - q m fits 24 bits, so that one fma and a comparison of |e| with m / 2 settle it.
+// scaled by the power of two that brings m to [1, 2), t = 127 p has at most 23 significant bits (p is a
+// product of two bf16 numbers, or one), a candidate q = round(t / m) is at most one off, and the rest t - q m
+// fits 24 bits, so that one fma gives it exactly.  Only where |rest| reaches m / 2 is q a tie or wrong; the eight
+// values of a vector are looked at again if one of them, in any lane, is there.
 //
 // The norm: h = x + residual rounded to bf16 (the residual stream as it is kept), p = h w, r = 1 /
 // sqrt(mean h^2 + eps), y = p r.  p is exact in fp32 and r is common to a row, so the codes depend on
@@ -25,24 +26,38 @@ __device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0
 
 // what the 8-bit form of a row needs from its greatest magnitude (bits)
 struct Form {
-    float m, inv;   // scaled to [1, 2); 127 / m
-    int e;          // its exponent
-    bool zero;      // all codes 0: the row is zero, or holds what is no number
+    float m, inv, scale127;   // m scaled to [1, 2), 1 / m; 127 times the scaling
+    int e;                    // its exponent
+    bool far;                 // the scaling is no fp32 number
     __device__ __forceinline__ explicit Form(uint32_t bits) {
-        zero = bits == 0 || bits >= 0x7F800000u;
-        const float v = zero ? 1.f : __uint_as_float(bits);
+        // (a row of zeros, or one that holds what is no number: all codes 0)
+        const bool none = bits == 0 || bits >= 0x7F800000u;
+        const float v = none ? 1.f : __uint_as_float(bits);
         e = 1 - __builtin_amdgcn_frexp_expf(v);
         m = ldexpf(v, e);
-        inv = 127.f / m;
+        inv = 1.f / m;
+        far = e > 100 || e < -100;
+        scale127 = none ? 0.f : ldexpf(127.f, far ? 0 : e);
     }
-    // the code of p, |p| <= m: a whole number
-    __device__ __forceinline__ float code(float p) const {
-        const float t = __builtin_amdgcn_ldexpf(p, e);
-        const float q = rintf(t * inv);
-        const float rest = fmaf(-q, m, 127.f * t), far = fabsf(rest), half = 0.5f * m;
-        const bool odd = ((int)q & 1) != 0;
-        const float r = (far > half || (far == half && odd)) ? q + copysignf(1.f, rest) : q;
-        return zero ? 0.f : r;
+    // the codes of eight values of the row, whole numbers
+    __device__ __forceinline__ void codes(const float (&p)[8], float (&q)[8]) const {
+        bool edge = false;
+        float rest[8];
+        const float half = 0.5f * m;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float t = far ? ldexpf(p[i], e) * 127.f : p[i] * scale127;      // (the same for the whole row)
+            q[i] = rintf(t * inv);
+            rest[i] = fmaf(-q[i], m, t);
+            edge |= fabsf(rest[i]) >= half;
+        }
+        if (__any(edge)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float r = fabsf(rest[i]);
+                if (r > half || (r == half && ((int)q[i] & 1) != 0)) q[i] += copysignf(1.f, rest[i]);
+            }
+        }
     }
 };
 
@@ -80,16 +95,16 @@ __device__ __forceinline__ const bf16_t* row_of(const void* p, int64_t row, int6
 // codes and held values of the eight values p of vector v of a row
 __device__ __forceinline__ void put_form(const RowsArgs& a, int64_t row, int v, const float (&p)[8], const Form& f, float scale) {
     float q[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = f.code(p[e]);
+    f.codes(p, q);
     if (a.code) {
         u32x2 c;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-            uint32_t b = 0;
+            uint32_t b[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) b |= ((uint32_t)(int)q[4 * w + e] & 0xFFu) << (8 * e);
-            c[w] = b;
+            for (int e = 0; e < 4; ++e) b[e] = (uint32_t)(int)q[4 * w + e];      // (0 of what is no number)
+            c[w] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0C0C0400u),
+                                         __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u), 0x05040100u);
         }
         *reinterpret_cast<u32x2*>(a.code + row * a.d + v * 8) = c;
     }
@@ -232,8 +247,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rows_act_kernel(RowsArgs a)
     }
 }
 
-// Threads a row: a wave for rows of up to 1024 values; else the fewest vectors a thread that leave a
-// workgroup of at most 512 threads (1024 for the widest rows).
+// Threads a row: a wave for rows of up to 1024 values; else the fewest vectors a thread that leave a workgroup of at
+// most 512 threads, or 1024 where each row has a compute unit of its own (and for the widest rows).
 template <class Go>
 hipError_t by_width(const RowsArgs& a, Go go) {
     if (a.n_rows < 1 || a.d < 8 || a.d % 8 || a.d > kMaxRowWidth) return hipErrorInvalidValue;
@@ -244,12 +259,13 @@ hipError_t by_width(const RowsArgs& a, Go go) {
         return blocks <= kMost ? dim3((unsigned)blocks) : dim3((unsigned)kMost, (unsigned)((blocks + kMost - 1) / kMost));
     };
     const dim3 rows = grid(a.n_rows), fours = grid(((int64_t)a.n_rows + 3) / 4), four(256);
+    const int most = a.n_rows <= 256 ? 1024 : 512;
     if (vecs <= 64) go.template operator()<1, true>(fours, four);
     else if (vecs <= 128) go.template operator()<2, true>(fours, four);
-    else if (vecs <= 512) go.template operator()<1, false>(rows, waves(1));
-    else if (vecs <= 1024) go.template operator()<2, false>(rows, waves(2));
-    else if (vecs <= 1536) go.template operator()<3, false>(rows, waves(3));
-    else if (vecs <= 2048) go.template operator()<4, false>(rows, waves(4));
+    else if (vecs <= most) go.template operator()<1, false>(rows, waves(1));
+    else if (vecs <= 2 * most) go.template operator()<2, false>(rows, waves(2));
+    else if (vecs <= 3 * most) go.template operator()<3, false>(rows, waves(3));
+    else if (vecs <= 4 * most) go.template operator()<4, false>(rows, waves(4));
     else go.template operator()<8, false>(rows, waves(8));
     return hipGetLastError();
 }
