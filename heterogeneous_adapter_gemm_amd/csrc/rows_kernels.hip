@@ -11,9 +11,11 @@
 // sqrt(mean h^2 + eps), y = p r.  p is exact in fp32 and r is common to a row, so the codes depend on
 // neither the order of the sum of squares nor on r.
 //
-// Each row is read once: a workgroup (rows of up to 1024 values: a wave) holds it in registers from its
+// Each row is read once: a workgroup (narrow rows: some lanes of a wave) holds it in registers from its
 // loads to its stores, with one reduction in between.  The kernels are bound by memory: 16-byte loads and
 // stores of consecutive lanes.
+#include <type_traits>
+
 #include "act_device.h"
 #include "common.h"
 #include "rows.h"
@@ -61,15 +63,18 @@ struct Form {
     }
 };
 
-// sum and greatest bits over the row's threads: a wave, or the workgroup
-template <bool WAVE>
+// LANES: the lanes of a wave that hold a row (16, 32 or 64; a workgroup of 256 then holds 256 / LANES rows), or 0: the
+// workgroup holds one row.
+
+// sum and greatest bits over the row's threads
+template <int LANES>
 __device__ __forceinline__ void reduce(float& s, uint32_t& m) {
 #pragma unroll
-    for (int k = 32; k >= 1; k >>= 1) {
+    for (int k = (LANES ? LANES : 64) / 2; k >= 1; k >>= 1) {
         s += __shfl_xor(s, k, 64);
         m = max(m, (uint32_t)__shfl_xor((int)m, k, 64));
     }
-    if constexpr (!WAVE) {
+    if constexpr (LANES == 0) {
         __shared__ float ps[16];
         __shared__ uint32_t pm[16];
         const int wave = threadIdx.x >> 6, n = blockDim.x >> 6;
@@ -115,19 +120,20 @@ __device__ __forceinline__ void put_form(const RowsArgs& a, int64_t row, int v, 
     }
 }
 
-// the row of this wave or workgroup (the grid has a second dimension where its threads would pass 32 bits)
-template <bool WAVE>
+// the row of this thread (the grid has a second dimension where its threads would pass 32 bits)
+template <int LANES>
 __device__ __forceinline__ int64_t row_here() {
     const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-    return WAVE ? block * 4 + (threadIdx.x >> 6) : block;
+    if constexpr (LANES == 0) return block;
+    else return block * (256 / LANES) + threadIdx.x / LANES;
 }
 
-// NV vectors of 8 values a thread; WAVE: a wave a row and four rows a workgroup, else a workgroup a row
-template <int NV, bool WAVE>
-__global__ __launch_bounds__(WAVE ? 256 : 1024) void rows_norm_kernel(RowsArgs a) {
-    const int64_t row = row_here<WAVE>();
+// NV vectors of 8 values a thread
+template <int NV, int LANES>
+__global__ __launch_bounds__(LANES ? 256 : 1024) void rows_norm_kernel(RowsArgs a) {
+    const int64_t row = row_here<LANES>();
     if (row >= a.n_rows) return;
-    const int t = WAVE ? threadIdx.x & 63 : threadIdx.x, nt = WAVE ? 64 : blockDim.x, vecs = a.d >> 3;
+    const int t = LANES ? threadIdx.x % LANES : threadIdx.x, nt = LANES ? LANES : blockDim.x, vecs = a.d >> 3;
     const u32x4 none = {0u, 0u, 0u, 0u};
     u32x4 h[NV], w[NV];
     const bf16_t* x = row_of(a.x, row, a.x_stride);
@@ -170,7 +176,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rows_norm_kernel(RowsArgs a
             m = max(m, mag(p[e] * g[e]));
         }
     }
-    reduce<WAVE>(ss, m);
+    reduce<LANES>(ss, m);
     // squares past fp32's range leave no norm: the row is NaN, as one that holds an infinity or NaN is
     const float r = ss < INFINITY ? 1.f / sqrtf(ss / (float)a.d + a.eps) : NAN;
     const Form f(m);
@@ -194,11 +200,11 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rows_norm_kernel(RowsArgs a
     }
 }
 
-template <int NV, bool WAVE, int ACT>
-__global__ __launch_bounds__(WAVE ? 256 : 1024) void rows_act_kernel(RowsArgs a) {
-    const int64_t row = row_here<WAVE>();
+template <int NV, int LANES, int ACT>
+__global__ __launch_bounds__(LANES ? 256 : 1024) void rows_act_kernel(RowsArgs a) {
+    const int64_t row = row_here<LANES>();
     if (row >= a.n_rows) return;
-    const int t = WAVE ? threadIdx.x & 63 : threadIdx.x, nt = WAVE ? 64 : blockDim.x, vecs = a.d >> 3;
+    const int t = LANES ? threadIdx.x % LANES : threadIdx.x, nt = LANES ? LANES : blockDim.x, vecs = a.d >> 3;
     const u32x4 none = {0u, 0u, 0u, 0u};
     u32x4 h[NV], gv[NV];
     const bf16_t* x = row_of(a.x, row, a.x_stride);
@@ -233,7 +239,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rows_act_kernel(RowsArgs a)
     }
     if (!a.code && !a.held) return;
     float unused = 0.f;
-    reduce<WAVE>(unused, m);
+    reduce<LANES>(unused, m);
     const Form f(m);
     const float scale = m < 0x7F800000u ? __uint_as_float(m) / 127.f : NAN;
     if (a.scale && t == 0) a.scale[row] = scale;
@@ -247,35 +253,56 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rows_act_kernel(RowsArgs a)
     }
 }
 
-// Threads a row: a wave for rows of up to 1024 values; else the fewest vectors a thread that leave a workgroup of at
-// most 512 threads, or 1024 where each row has a compute unit of its own (and for the widest rows).
-template <class Go>
+// Threads a row: 16, 32 or 64 lanes for rows of up to 1024 values; else the fewest vectors a thread that leave a
+// workgroup of at most 512 threads, or 1024 where each row has a compute unit of its own (and for the widest rows).
+// The norm of many rows of up to 4096 values is faster a wave a row, from about 8 rows a compute unit on (3,000 x 4096:
+// 25.6 us against 28.7; 1,000 rows 11.9 against 11.5; act 27.4 against 23.7).
+template <bool NORM, class Go>
 hipError_t by_width(const RowsArgs& a, Go go) {
     if (a.n_rows < 1 || a.d < 8 || a.d % 8 || a.d > kMaxRowWidth) return hipErrorInvalidValue;
     const int vecs = a.d / 8;
-    auto waves = [&](int nv) { return dim3((vecs + nv * 64 - 1) / (nv * 64) * 64); };
     auto grid = [](int64_t blocks) {
         constexpr int64_t kMost = 1 << 20;
         return blocks <= kMost ? dim3((unsigned)blocks) : dim3((unsigned)kMost, (unsigned)((blocks + kMost - 1) / kMost));
     };
-    const dim3 rows = grid(a.n_rows), fours = grid(((int64_t)a.n_rows + 3) / 4), four(256);
+    auto lanes = [&](auto nv, auto l) {
+        constexpr int NV = decltype(nv)::value, LANES = decltype(l)::value, ROWS = 256 / LANES;
+        go.template operator()<NV, LANES>(grid(((int64_t)a.n_rows + ROWS - 1) / ROWS), dim3(256));
+    };
+    auto wide = [&](auto nv) {
+        constexpr int NV = decltype(nv)::value;
+        go.template operator()<NV, 0>(grid(a.n_rows), dim3((vecs + NV * 64 - 1) / (NV * 64) * 64));
+    };
+    using std::integral_constant;
+    const integral_constant<int, 1> one;
+    const integral_constant<int, 2> two;
+    const integral_constant<int, 4> four;
+    const integral_constant<int, 8> eight;
     const int most = a.n_rows <= 256 ? 1024 : 512;
-    if (vecs <= 64) go.template operator()<1, true>(fours, four);
-    else if (vecs <= 128) go.template operator()<2, true>(fours, four);
-    else if (vecs <= most) go.template operator()<1, false>(rows, waves(1));
-    else if (vecs <= 2 * most) go.template operator()<2, false>(rows, waves(2));
-    else if (vecs <= 3 * most) go.template operator()<3, false>(rows, waves(3));
-    else if (vecs <= 4 * most) go.template operator()<4, false>(rows, waves(4));
-    else go.template operator()<8, false>(rows, waves(8));
+    const bool many = NORM && a.n_rows >= 2048;
+    if (vecs <= 16) lanes(one, integral_constant<int, 16>{});
+    else if (vecs <= 32) lanes(one, integral_constant<int, 32>{});
+    else if (vecs <= 64) lanes(one, integral_constant<int, 64>{});
+    else if (vecs <= 128) lanes(two, integral_constant<int, 64>{});
+    else if (many && vecs <= 512) {
+        if constexpr (NORM) {
+            if (vecs <= 256) lanes(four, integral_constant<int, 64>{});
+            else lanes(eight, integral_constant<int, 64>{});
+        }
+    } else if (vecs <= most) wide(one);
+    else if (vecs <= 2 * most) wide(two);
+    else if (vecs <= 3 * most) wide(integral_constant<int, 3>{});
+    else if (vecs <= 4 * most) wide(four);
+    else wide(eight);
     return hipGetLastError();
 }
 
 struct GoNorm {
     const RowsArgs& a;
     hipStream_t s;
-    template <int NV, bool WAVE>
+    template <int NV, int LANES>
     void operator()(dim3 grid, dim3 block) const {
-        hipLaunchKernelGGL((rows_norm_kernel<NV, WAVE>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((rows_norm_kernel<NV, LANES>), grid, block, 0, s, a);
     }
 };
 
@@ -283,22 +310,22 @@ template <int ACT>
 struct GoAct {
     const RowsArgs& a;
     hipStream_t s;
-    template <int NV, bool WAVE>
+    template <int NV, int LANES>
     void operator()(dim3 grid, dim3 block) const {
-        hipLaunchKernelGGL((rows_act_kernel<NV, WAVE, ACT>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((rows_act_kernel<NV, LANES, ACT>), grid, block, 0, s, a);
     }
 };
 
 }  // namespace
 
-hipError_t launch_rows_norm(const RowsArgs& a, hipStream_t s) { return by_width(a, GoNorm{a, s}); }
+hipError_t launch_rows_norm(const RowsArgs& a, hipStream_t s) { return by_width<true>(a, GoNorm{a, s}); }
 
 hipError_t launch_rows_act(const RowsArgs& a, int act, hipStream_t s) {
     switch (act) {
-        case kActNone: return by_width(a, GoAct<kActNone>{a, s});
-        case kActSilu: return by_width(a, GoAct<kActSilu>{a, s});
-        case kActGelu: return by_width(a, GoAct<kActGelu>{a, s});
-        case kActGeluTanh: return by_width(a, GoAct<kActGeluTanh>{a, s});
+        case kActNone: return by_width<false>(a, GoAct<kActNone>{a, s});
+        case kActSilu: return by_width<false>(a, GoAct<kActSilu>{a, s});
+        case kActGelu: return by_width<false>(a, GoAct<kActGelu>{a, s});
+        case kActGeluTanh: return by_width<false>(a, GoAct<kActGeluTanh>{a, s});
         default: return hipErrorInvalidValue;
     }
 }

@@ -55,8 +55,8 @@ def check_form(code, scale, held, want_code, want_scale, rel, n):
         assert np.all(np.abs(to_np(held) - v) <= np.abs(v) * (E.HALF + 2 * E.ULP) + E.TINY)
 
 
-# widths of every kind of row: a wave's (one and two vectors a lane), a workgroup's with 1, 2, 3, 4 and 8
-WIDTHS = [8, 64, 72, 512, 520, 1024, 1032, 4096, 4104, 5120, 8192, 8200, 11008, 12288, 12296, 16384, 16392, 28672, 65536]
+# widths of every kind of row: 16, 32 and 64 lanes' (one and two vectors a lane), a workgroup's with 1, 2, 3, 4 and 8
+WIDTHS = [8, 64, 72, 128, 136, 256, 264, 512, 520, 1024, 1032, 4096, 4104, 5120, 8192, 8200, 11008, 12288, 12296, 16384, 16392, 28672, 65536]
 
 
 @pytest.mark.parametrize("d", WIDTHS)
@@ -198,9 +198,9 @@ def test_some_outputs_only_and_in_place(d):
 
 
 def test_many_rows():
-    """More rows than a round of workgroups, of both kinds of rows; an odd count of a wave's rows."""
+    """More rows than a round of workgroups; odd counts of a wave's rows; the norm's wave a row."""
     import heterogeneous_adapter_gemm_amd as hg
-    for n, d in ((20003, 128), (9001, 1032)):
+    for n, d in ((20003, 128), (9001, 1032), (4001, 200), (2049, 2048), (2500, 2056), (2048, 4096), (3001, 4104)):
         say("many rows", n, d)
         g = np.random.default_rng(n)
         x = E.bf16(g.standard_normal((n, d)))
