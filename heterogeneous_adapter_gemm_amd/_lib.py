@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import numpy as np
@@ -144,8 +145,8 @@ _SIGS = {
     "lora_linear_fp8": [_VP, _VP, ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP],
     "base_gemm_w4": [_VP, _VP, _VP, _VP, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _VP],
     "lora_linear_w4": [_VP, _VP, ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP, ctypes.c_int32, _VP, _VP],
-    "rows_norm_i8": [ctypes.POINTER(lora_norm_rows), _VP],
-    "rows_act_i8": [ctypes.POINTER(lora_act_rows), _VP],
+    "rows_norm_i8": [_VP, _VP],     # lora_norm_rows *, lora_act_rows * (or their bytes)
+    "rows_act_i8": [_VP, _VP],
     "base_gemm_i8": [_VP, _VP, _VP, _VP, _VP, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _VP],
     "base_gated_i8": [_VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int32, _VP, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _VP],
     "lora_linear_i8": [_VP, _VP, ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP, _VP, _VP],
@@ -556,22 +557,28 @@ def _row_shape(x):
 def _rows(name: str, t, shape, dev: int):
     """Address and row stride of bf16 rows of a shape on a GPU (None: NULL)."""
     if t is None:
-        return None, 0
-    row, one = t.stride() if t.dim() == 2 else (0, 0)
-    if one != 1 or t.shape != shape or t.dtype is not _BF16 or t.get_device() != dev:
-        raise ValueError(f"{name}: bfloat16 rows {list(shape)}, contiguous along a row, on the GPU of x are needed")
-    return t.data_ptr(), row
+        return 0, 0
+    if t.shape == shape and t.dtype is _BF16 and t.get_device() == dev:
+        row, one = t.stride()
+        if one == 1:
+            return t.data_ptr(), row
+    raise ValueError(f"{name}: bfloat16 rows {list(shape)}, contiguous along a row, on the GPU of x are needed")
 
 
 def _form(code, scale, shape, dev: int):
     """Addresses of the codes [n, d] and scales [n] of rows (both None: NULL)."""
     if code is None and scale is None:
-        return None, None
+        return 0, 0
     if code is None or scale is None or code.shape != shape or code.dtype is not _INT8 or scale.dtype is not _FP32 or \
-            scale.dim() != 1 or scale.shape[0] != shape[0] or code.get_device() != dev or scale.get_device() != dev or \
+            scale.numel() != shape[0] or code.get_device() != dev or scale.get_device() != dev or \
             not code.is_contiguous() or not scale.is_contiguous():
         raise ValueError(f"code and scale: contiguous int8 {list(shape)} and float32 [{shape[0]}] on the GPU of x, together")
     return code.data_ptr(), scale.data_ptr()
+
+
+# the C structs' bytes: a ctypes.Structure takes 0.3 us to fill, a pack 0.1
+_NORM_ROWS = struct.Struct("@qif8P5q")
+_ACT_ROWS = struct.Struct("@qii6P4q")
 
 
 def _rows_call(name: str, rows, dev: int, stream) -> None:
@@ -593,8 +600,7 @@ def rows_norm_i8(x, weight, eps: float, residual=None, sum_out=None, y=None, cod
                  stream=None) -> None:
     """Norm of bf16 rows x (+ residual) [n, d] with the weight [d]: y, and the 8-bit form code, scale, held."""
     shape, dev = _row_shape(x)
-    if weight.dtype is not _BF16 or weight.dim() != 1 or weight.shape[0] != shape[1] or weight.get_device() != dev or \
-            not weight.is_contiguous():
+    if weight.dtype is not _BF16 or weight.numel() != shape[1] or weight.get_device() != dev or not weight.is_contiguous():
         raise ValueError(f"weight: contiguous bfloat16 [{shape[1]}] on the GPU of x is needed")
     xp, xs = _rows("x", x, shape, dev)
     rp, rs = _rows("residual", residual, shape, dev)
@@ -602,8 +608,8 @@ def rows_norm_i8(x, weight, eps: float, residual=None, sum_out=None, y=None, cod
     yp, ys = _rows("y", y, shape, dev)
     hp, hs = _rows("held", held, shape, dev)
     cp, fp = _form(code, scale, shape, dev)
-    _rows_call("rows_norm_i8", lora_norm_rows(shape[0], shape[1], eps, xp, rp, weight.data_ptr(), sp, yp, hp, cp, fp, xs, rs,
-                                              ss, ys, hs), dev, stream)
+    _rows_call("rows_norm_i8", _NORM_ROWS.pack(shape[0], shape[1], eps, xp, rp, weight.data_ptr(), sp, yp, hp, cp, fp, xs, rs,
+                                               ss, ys, hs), dev, stream)
 
 
 def _act(act) -> int:
@@ -624,7 +630,7 @@ def rows_act_i8(x, gate=None, act="none", y=None, code=None, scale=None, held=No
     yp, ys = _rows("y", y, shape, dev)
     hp, hs = _rows("held", held, shape, dev)
     cp, fp = _form(code, scale, shape, dev)
-    _rows_call("rows_act_i8", lora_act_rows(shape[0], shape[1], act, xp, gp, yp, hp, cp, fp, xs, gs, ys, hs), dev, stream)
+    _rows_call("rows_act_i8", _ACT_ROWS.pack(shape[0], shape[1], act, xp, gp, yp, hp, cp, fp, xs, gs, ys, hs), dev, stream)
 
 
 def base_gemm_i8(x_code, x_scale, w0_code, w0_scale, y, M: int, N: int, K: int, stream=None) -> None:

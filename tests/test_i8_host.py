@@ -119,6 +119,12 @@ def test_rows_of_tensors_are_checked():
         hg.base_gated_i8(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 4, 64, 64, act="tanh")
 
 
+def test_packed_rows_are_the_structs():
+    for packed, c in ((_lib._NORM_ROWS, hg.lora_norm_rows), (_lib._ACT_ROWS, hg.lora_act_rows)):
+        v = [3, 40, 5] + list(range(1 << 40, (1 << 40) + len(c._fields_) - 3))
+        assert packed.size == ctypes.sizeof(c) and packed.pack(*v) == bytes(c(*v))
+
+
 def test_codes_by_whole_numbers():
     """The oracle's codes against whole-number arithmetic: p and max|p| as integers of one unit."""
     g = np.random.default_rng(5)
