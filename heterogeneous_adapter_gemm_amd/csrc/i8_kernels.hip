@@ -476,9 +476,11 @@ __global__ __launch_bounds__(kLongWaves * 64, 1) void i8_long_kernel(I8Args g, L
     }
 }
 
-// The kinds of tiles.  Up to 64 x 64 the stream's, above it the long ones.
+// The kinds of tiles.  The stream's rings are short: room for a second workgroup in a compute unit does more than a
+// longer ring (64 x 4096 x 4096 in 32 x 32 tiles 7.9 us with two stages, 8.3 with four; 64 -> 11008 in 32 x 48 16.5
+// and 18.9; one row in 16 x 16 5.3 with two, 5.2 with four, 5.7 with eight).
 template <int FM, int FN>
-using Stream = StreamCfg<FM, FN, (FM == 1 && FN == 1) ? 8 : (FM + FN <= 5) ? 4 : (FM + FN == 6) ? 3 : 2>;
+using Stream = StreamCfg<FM, FN, FM + FN == 2 ? 4 : 2>;
 using Long64 = LongCfg<64, 64, 5, 5>;
 using Long128x64 = LongCfg<128, 64, 4, 4>;
 using Long128 = LongCfg<128, 128, 4, 4>;
