@@ -1,5 +1,4 @@
-// The prefill rows' LoRA expand inside a GEMM tile, shared by the long-batch tiles of the bf16 and the
-// 8-bit base.
+// The prefill rows' LoRA expand inside a GEMM tile: of the bf16 base's long-batch tiles, and of the 8-bit base's.
 #pragma once
 
 #include "common.h"
@@ -105,5 +104,94 @@ __device__ __forceinline__ void expand_segments(const LoraArgs& seg, int m0, int
         }
     }
 }
+
+// The same expand, its global reads ahead of their use: the next 32-wide slice of a rank (of the same or the next
+// overlapping segment) is read into registers while the matrix cores work on the one in LDS, the first one behind the
+// base product's loop while its sums are scaled, and which segment that is before the loop.  (The first slice's values
+// themselves before the loop: 24 registers, which the compiler put into scratch memory.)
+template <int BM, int BN, int NT>
+struct ExpandSlices {
+    static constexpr int LDJ = kExpandRow;
+    static constexpr int IB = (16 * (BN / 8) + NT - 1) / NT;     // items of a thread: a pair of rank-rows, 8 columns
+    static constexpr int IV = (BM * 4 + NT - 1) / NT;            // a row of v, 8 of the slice's rank
+    u32x4 b0[IB], b1[IB];
+    f32x4 v[IV][2];
+    const int32_t* tab;
+    float gamma;
+    int s = -1, r = 0, jb = 0, sb = 0, se = 0;
+    bool live = false;
+
+    // to the next slice that the tile's rows m0 .. need (the same for the whole workgroup)
+    __device__ __forceinline__ void next(const LoraArgs& seg, int m0) {
+        jb += 32;
+        if (jb < r) return;
+        jb = 0;
+        live = false;
+        while (++s < seg.n_segs) {
+            sb = seg.s_begin[s];
+            se = seg.s_end[s];
+            if (se <= m0 || sb >= m0 + BM || sb >= se) continue;
+            r = seg.s_rank[s];
+            gamma = seg.s_gamma[s];
+            tab = seg.page_tab + (int64_t)seg.s_slot[s] * seg.slot_cap + (int64_t)r * seg.lp_per_rank + r * seg.nci;
+            live = true;
+            return;
+        }
+    }
+    __device__ __forceinline__ void load(const LoraArgs& seg, int m0, int n0, int N) {
+        const int pmask = (1 << seg.page_shift) - 1;
+#pragma unroll
+        for (int i = 0; i < IB; ++i) {
+            const int idx = threadIdx.x + i * NT, jp = idx & 15, nv = idx >> 4;
+            const int n = min(n0 + nv * 8, N - 8), pg = n >> seg.page_shift, po = n & pmask, j0 = jb + 2 * jp;
+            const bf16_t* pages = static_cast<const bf16_t*>(seg.pages);
+            b0[i] = ld16(pages + ((int64_t)tab[min(j0, r - 1) * seg.nco + pg] << seg.page_shift) + po);
+            b1[i] = ld16(pages + ((int64_t)tab[min(j0 + 1, r - 1) * seg.nco + pg] << seg.page_shift) + po);
+        }
+#pragma unroll
+        for (int i = 0; i < IV; ++i) {
+            // (a row outside the segment, or a thread past the tile's rows: some row of it, not used)
+            const int idx = threadIdx.x + i * NT, m = max(sb, min(m0 + (idx >> 2), se - 1));
+            const float* vp = seg.v + (int64_t)m * seg.vstride + jb + (idx & 3) * 8;
+            const bool in = jb + (idx & 3) * 8 < r;      // (v's rows end behind the rank, rounded up to 8)
+            v[i][0] = in ? *reinterpret_cast<const f32x4*>(vp) : f32x4{0.f, 0.f, 0.f, 0.f};
+            v[i][1] = in ? *reinterpret_cast<const f32x4*>(vp + 4) : f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+    }
+    // the slice in registers to LDS (layouts as for expand_segments)
+    __device__ __forceinline__ void store(int m0, int n0, int N, uint16_t* bt, uint16_t* vh, uint16_t* vl) const {
+        uint32_t* btw = reinterpret_cast<uint32_t*>(bt);
+#pragma unroll
+        for (int i = 0; i < IB; ++i) {
+            const int idx = threadIdx.x + i * NT, jp = idx & 15, nv = idx >> 4, j0 = jb + 2 * jp;
+            if (16 * (BN / 8) % NT != 0 && nv >= BN / 8) continue;
+            const bool nin = n0 + nv * 8 < N, in0 = nin && j0 < r, in1 = nin && j0 + 1 < r;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t w0 = in0 ? b0[i][e] : 0u, w1 = in1 ? b1[i][e] : 0u;
+                btw[(nv * 8 + 2 * e) * (LDJ / 2) + jp] = (w0 & 0xFFFFu) | (w1 << 16);
+                btw[(nv * 8 + 2 * e + 1) * (LDJ / 2) + jp] = (w0 >> 16) | (w1 & 0xFFFF0000u);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < IV; ++i) {
+            const int idx = threadIdx.x + i * NT, ml = idx >> 2, j = (idx & 3) * 8, m = m0 + ml;
+            if (BM * 4 % NT != 0 && ml >= BM) continue;
+            const bool in = m >= sb && m < se;
+            float a[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a[e] = in && jb + j + e < r ? gamma * v[i][e >> 2][e & 3] : 0.f;
+            u32x4 hi, lo;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t h0 = f32_to_bf16(a[2 * e]), h1 = f32_to_bf16(a[2 * e + 1]);
+                hi[e] = h0 | (h1 << 16);
+                lo[e] = pack_bf16(a[2 * e] - __uint_as_float(h0 << 16), a[2 * e + 1] - __uint_as_float(h1 << 16));
+            }
+            *reinterpret_cast<u32x4*>(&vh[ml * LDJ + j]) = hi;
+            *reinterpret_cast<u32x4*>(&vl[ml * LDJ + j]) = lo;
+        }
+    }
+};
 
 }  // namespace hagemm

@@ -390,6 +390,7 @@ __global__ __launch_bounds__(kLongWaves * 64, 1) void i8_long_kernel(I8Args g, L
         half(xs_of(nx), ws_of(nw), f0, xc, xa);
         order(std::integral_constant<int, LPB>{});
     };
+    ExpandSlices<BM, BN, NW * 64> slices;
     constexpr int U = SX == SW ? SX : SX * SW;     // steps after which both rings are where they were
     const int nk = (K + RB - 1) / RB;
     constexpr int S1 = SX > SW ? SX : SW;
@@ -399,6 +400,7 @@ __global__ __launch_bounds__(kLongWaves * 64, 1) void i8_long_kernel(I8Args g, L
         if (j + SX >= 0) issue_x(j + SX, xs_of(j + SX));
         if (SW > SX && j + SW >= 0) issue_w(j + SW, ws_of(j + SW));
     }
+    if constexpr (FUSE) slices.next(seg, m0);
     wait_vmcnt<OPEN>();
     __builtin_amdgcn_s_barrier();
     refill(-1, SX - 1, SW - 1);
@@ -415,6 +417,9 @@ __global__ __launch_bounds__(kLongWaves * 64, 1) void i8_long_kernel(I8Args g, L
     for (int u = 0; u < U - 1; ++u)
         if (full + u < nk) step(full + u, u % SX, u % SW, (u + 1) % SX, (u + 1) % SW);
     wait_vmcnt<0>();   // no load may still be writing LDS
+    if constexpr (FUSE) {
+        if (slices.live) slices.load(seg, m0, n0, N);
+    }
 
     // lane holds D[n = 4 lg + i][m = li] of each block (rows and columns past the end: the last ones' scales)
     constexpr int FO = GATED ? FN / 2 : FN, OC = FO * 16;      // output columns of a wave
@@ -429,9 +434,31 @@ __global__ __launch_bounds__(kLongWaves * 64, 1) void i8_long_kernel(I8Args g, L
         for (int b = 0; b < FM; ++b) acc[a][b] = scaled(__builtin_bit_cast(i32x4, acc[a][b]), xs[b], ws);
     }
     if constexpr (FUSE) {
-        static_assert(kExpandRow * 2 <= RB, "the expand's operands");
-        expand_segments<BM, BN, WM, WN>(seg, m0, n0, N, reinterpret_cast<uint16_t*>(ldw0), reinterpret_cast<uint16_t*>(ldx0),
-                                        reinterpret_cast<uint16_t*>(ldx1), acc);
+        constexpr int LDJ = kExpandRow;
+        static_assert(LDJ * 2 <= RB, "the expand's operands");
+        uint16_t *bt = reinterpret_cast<uint16_t*>(ldw0), *vh = reinterpret_cast<uint16_t*>(ldx0), *vl = reinterpret_cast<uint16_t*>(ldx1);
+        while (slices.live) {
+            __syncthreads();   // the LDS is free: of the product, or of the slice before
+            slices.store(m0, n0, N, bt, vh, vl);
+            slices.next(seg, m0);
+            if (slices.live) slices.load(seg, m0, n0, N);
+            __syncthreads();
+            u32x4 hi[FM], lo[FM];
+#pragma unroll
+            for (int b = 0; b < FM; ++b) {
+                hi[b] = *reinterpret_cast<const u32x4*>(&vh[(wm * WTM + b * 16 + li) * LDJ + 8 * lg]);
+                lo[b] = *reinterpret_cast<const u32x4*>(&vl[(wm * WTM + b * 16 + li) * LDJ + 8 * lg]);
+            }
+#pragma unroll
+            for (int a = 0; a < FN; ++a) {
+                const u32x4 bf = *reinterpret_cast<const u32x4*>(&bt[(wn * WTN + a * 16 + li) * LDJ + 8 * lg]);
+#pragma unroll
+                for (int b = 0; b < FM; ++b) {
+                    acc[a][b] = mma_step(bf, hi[b], acc[a][b], bf16_t{});
+                    acc[a][b] = mma_step(bf, lo[b], acc[a][b], bf16_t{});
+                }
+            }
+        }
     }
     // The outputs go through LDS, each wave's in a place of its own, so that a store instruction writes whole lines of
     // rows: straight from the lanes (8 bytes of each of 32 rows) the stores took 18 us of a tile's 70.  Rows whose
