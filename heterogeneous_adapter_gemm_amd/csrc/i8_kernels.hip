@@ -522,8 +522,8 @@ struct Kind {
 };
 constexpr Kind kKinds[] = {
     {16, 16, true}, {16, 32, true}, {16, 48, true}, {16, 64, true}, {16, 96, true},
-    {32, 16, true}, {32, 32, true}, {32, 48, true}, {32, 64, true}, {32, 96, true},
-    {64, 16, true}, {64, 32, true}, {64, 48, true}, {64, 64, true}, {64, 96, true},
+    {32, 32, true}, {32, 48, true}, {32, 64, true}, {32, 96, true},
+    {64, 48, true}, {64, 64, true}, {64, 96, true},
     {64, 64, false}, {128, 64, false}, {128, 128, false}, {192, 128, false}, {256, 128, false}, {192, 256, false}, {256, 256, false}};
 
 int64_t tiles_of(const I8Args& g, const Kind& k, bool two) {
@@ -611,8 +611,10 @@ void with_stream(const Kind& k, Go go) {
     auto by_rows = [&](auto fnc) {
         constexpr int FN = decltype(fnc)::value;
         if (k.bm == 16) go(Stream<1, FN>{});
-        else if (k.bm == 32) go(Stream<2, FN>{});
-        else go(Stream<4, FN>{});
+        else if constexpr (FN > 1) {
+            if (k.bm == 32) go(Stream<2, FN>{});
+            else if constexpr (FN > 2) go(Stream<4, FN>{});
+        }
     };
     if (k.bn == 32) by_rows(std::integral_constant<int, 2>{});
     else if (k.bn == 64) by_rows(std::integral_constant<int, 4>{});

@@ -39,13 +39,15 @@ def exact_product(x, w):
     return (p * gpu(x[1]).double()[:, None] * gpu(w[1]).double()).cpu().numpy()
 
 
-# rows in blocks of 16, 32 and 64 and several of them; 1 to 4 column blocks a tile; K of part of a slice, part of a
-# wave's step, several rings; then long tiles: 192 and 256 rows, alone and with a last round of 2, 4, 8 and 16 pieces
+# one row to several row blocks and column blocks of every kind of tile, K of part of a slice, part of a wave's step and
+# several rings; then each of the kinds that few sizes take, and last rounds of 2, 4, 8 and 16 pieces
 SHAPES = [(1, 4, 16), (1, 4096, 4096), (3, 100, 48), (16, 4160, 1040), (17, 36, 128), (16, 9000, 272), (5, 12800, 528), (32, 520, 2064),
           (30, 9000, 400), (31, 12300, 1024), (32, 16400, 640), (33, 260, 144), (64, 4096, 4096), (64, 8200, 384), (64, 10244, 2048),
           (48, 16388, 560), (64, 11008, 4112), (65, 1000, 768), (128, 4100, 656), (200, 4096, 1552), (256, 4096, 11008), (255, 7004, 352),
           (257, 64, 16), (300, 272, 656), (700, 4100, 304), (1000, 4096, 512), (2049, 8100, 272), (2961, 4096, 4096), (1100, 13000, 208),
-          (1500, 11008, 336), (4100, 4360, 160), (4352, 4128, 320), (2816, 6300, 592)]
+          (1500, 11008, 336), (4100, 4360, 160), (4352, 4128, 320), (2816, 6300, 592),
+          (1, 17036, 272), (33, 12316, 272), (19, 8472, 272), (8429, 72, 272), (151, 16500, 272), (206, 18732, 272),
+          (342, 48388, 608), (386, 43812, 944), (391, 70364, 288), (1167, 14356, 800), (754, 21900, 560)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -69,7 +71,9 @@ def test_product(M, N, K):
 
 GATED = [(1, 4, 16), (1, 11008, 4096), (16, 100, 48), (20, 4100, 400), (32, 2060, 2064), (64, 11008, 1040), (64, 260, 144), (64, 2052, 4096),
          (130, 1000, 768), (256, 4100, 656), (257, 132, 16), (700, 4100, 304), (1000, 2048, 512), (2049, 4060, 272), (2961, 2048, 2048),
-         (1100, 6500, 208), (1500, 5504, 336), (2816, 3156, 592), (4352, 2064, 320)]
+         (1100, 6500, 208), (1500, 5504, 336), (2816, 3156, 592), (4352, 2064, 320),
+         (1, 4148, 288), (17, 4216, 272), (33, 4300, 304), (34, 6264, 320), (8903, 36, 272), (163, 8552, 272),
+         (1026, 8052, 608), (388, 21844, 960), (385, 35172, 288), (471, 17564, 800), (758, 10884, 560)]
 
 
 @pytest.mark.parametrize("M,N,K", GATED)
@@ -209,11 +213,23 @@ def test_decode_rows_with_adapters(n, d_in, d_out, n_ad):
                                                    ([130, 1, 0, 77], 145, 1024, 1040), ([300, 212], 0, 512, 4104), ([64, 700, 33, 400], 192, 784, 2056),
                                                    ([1024, 900, 61], 64, 512, 4096), ([513, 1, 1, 640], 7, 4096, 1048)])
 def test_prompts_with_adapters(lens, n_dec, d_in, d_out):
+    prompts(lens, n_dec, d_in, d_out)
+
+
+# kinds of tiles that few sizes take, and last rounds of pieces, with the expand in the epilogue
+@pytest.mark.parametrize("lens,n_dec,d_in,d_out", [([100, 77, 40, 60], 12, 272, 11336), ([262], 0, 304, 16824), ([404], 0, 304, 23224),
+                                                   ([70, 300, 130, 80], 8, 272, 8744), ([1000, 900, 33, 1200], 30, 608, 5224), ([130, 200, 33], 23, 960, 43680),
+                                                   ([385], 0, 304, 70288), ([190, 130, 64], 68, 800, 36584), ([2000, 1500, 700, 600], 30, 560, 3416)])
+def test_prompts_in_every_kind_of_tile(lens, n_dec, d_in, d_out):
+    prompts(lens, n_dec, d_in, d_out)
+
+
+def prompts(lens, n_dec, d_in, d_out):
     import heterogeneous_adapter_gemm_amd as hg
     say("prompts", lens, n_dec, d_in, d_out)
     g = np.random.default_rng(sum(lens) + d_out)
     ranks = [16, 64, 33, 8]
-    pool, ad = setup(g, d_in, d_out, ranks)
+    pool, ad = setup(g, d_in, d_out, ranks, max_tokens=8192)
     sad = np.array([[0, -1, 1, 2][i % 4] for i in range(len(lens))])
     dec = g.integers(-1, len(ranks), n_dec)
     who = np.concatenate([np.repeat(sad, lens), dec])
