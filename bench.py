@@ -47,6 +47,7 @@ DEFAULT_STEPS = {"c2": 5000, "c3": 2000, "c4": 500, "c5": 20}
 KERNEL_TIMING = (f"HIP events on the launch stream around the kernels of every {TIMING_PERIOD}th LoRA-linear "
                  "call inside the timed region (avg_us = event-measured launch duration)")
 BF16_PEAK_TFLOPS = 2500.0      # MI355X dense bf16 MFMA
+I8_PEAK_TOPS = 5000.0          # MI355X dense int8 MFMA
 STACK_STAGE_BYTES = 512 << 20  # the stack step's page-in staging area (a layer of the 16 cold adapters is ~56 MB)
 
 WORKLOADS = {
@@ -206,6 +207,14 @@ def main():
     ap.add_argument("--fp8-base", action="store_true",
                     help="c2 / c3 / c4: the base weight as E4M3 codes with a scale per output channel "
                          "(lora_linear_fp8); the adapters stay bf16")
+    ap.add_argument("--i8-base", action="store_true",
+                    help="c2 / c3 / c4: the base weight and the rows as 8-bit integers with a scale per output channel "
+                         "and per row, the rows' form made in the step (rows_act_i8, lora_linear_i8); the adapters "
+                         "stay bf16")
+    ap.add_argument("--i8-mlp", action="store_true",
+                    help="only time a Llama-7B feed-forward block in 8-bit integers without adapters (norm with the "
+                         "residual, gated product, the gated rows' form, down product) at 1, 64 and 2,961 rows, one JSON "
+                         "line")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--single-calls", action="store_true",
                     help="stack: one lora_linear call per projection (no shared shrink launches for q, k, v and "
@@ -275,6 +284,8 @@ def main():
         return run_gemm_vs_library(args)
     if args.peaks:
         return run_peaks(args)
+    if args.i8_mlp:
+        return run_i8_mlp(args)
     if cfg == "c5":
         return run_stack(args)
     R = args.rotate or {"c2": 16, "c3": 4, "c4": 4}[cfg]
@@ -296,6 +307,12 @@ def main():
         codes, scale = wl.w0_fp8()
         ws = torch.from_numpy(codes).to("cuda").unsqueeze(0).repeat(R, 1, 1).contiguous()
         ss = torch.from_numpy(scale).to("cuda").unsqueeze(0).repeat(R, 1).contiguous()
+    elif args.i8_base:
+        codes, scale = wl.w0_i8()
+        ws = torch.from_numpy(codes).to("cuda").unsqueeze(0).repeat(R, 1, 1).contiguous()
+        ss = torch.from_numpy(scale).to("cuda").unsqueeze(0).repeat(R, 1).contiguous()
+        xc = torch.empty((R, T, wl.d_in[0]), dtype=torch.int8, device="cuda")
+        xsc = torch.empty((R, (T + 3) // 4 * 4), dtype=torch.float32, device="cuda")   # (16-byte aligned rows)
     else:
         ws = hg.device_tensor(wl.w0()).unsqueeze(0).repeat(R, 1, 1).contiguous()
     ys = torch.empty((R, T, wl.d_out[0]), dtype=torch.bfloat16, device="cuda")
@@ -308,14 +325,17 @@ def main():
     st = torch.cuda.current_stream().cuda_stream
     xp = [xs[l].data_ptr() for l in range(R)]
     wp = [ws[l].data_ptr() for l in range(R)]
-    sp = [ss[l].data_ptr() for l in range(R)] if args.fp8_base else None
+    sp = [ss[l].data_ptr() for l in range(R)] if args.fp8_base or args.i8_base else None
     yp = [ys[l].data_ptr() for l in range(R)]
     idx_c = [(ix.get("seg_start"), ix.get("seg_slot"), ix.get("token_slot")) for ix in idx]
 
     def step(i):
         b, l = i % NB, i % R
         plan = pool.plan(*idx_c[b], stream=st)
-        if sp is not None:
+        if args.i8_base:
+            hg.rows_act_i8(xs[l], code=xc[l], scale=xsc[l, :T], stream=st)
+            pool.linear_i8(plan, l, 0, xp[l], xc[l].data_ptr(), xsc[l].data_ptr(), wp[l], sp[l], yp[l], stream=st)
+        elif sp is not None:
             pool.linear_fp8(plan, l, 0, xp[l], wp[l], sp[l], yp[l], stream=st)
         else:
             pool.linear(plan, l, 0, xp[l], wp[l], yp[l], stream=st)
@@ -349,8 +369,10 @@ def main():
         sb += s / NB
         eb += e / NB
         dist += d / NB
-    # (FP8 base: one byte per weight and a 4-byte scale per output channel)
-    gemm_bytes = (N * K + 4 * N if args.fp8_base else N * K * 2) + (M * K + M * N) * 2
+    # (FP8 and 8-bit base: one byte per weight and a 4-byte scale per output channel; 8-bit: and per row)
+    gemm_bytes = (N * K + 4 * N if args.fp8_base or args.i8_base else N * K * 2) + (M * K + M * N) * 2
+    if args.i8_base:
+        gemm_bytes += 4 * M - M * K
     gemm_flops = 2.0 * M * N * K
     alg = {"gemm": gemm_bytes, "bgmv_shrink": sb, "bgmv_expand": eb, "sgmv_shrink": sb, "sgmv_expand": eb,
            "gemm_bgmv_shrink": gemm_bytes + sb}
@@ -359,10 +381,11 @@ def main():
             k["alg_bytes"] = alg[name]
             k["GBps"] = alg[name] / (k["avg_us"] * 1e-6) / 1e9
             k["frac_hbm_peak"] = k["GBps"] / HBM_PEAK_GBS
+    mfma_peak = I8_PEAK_TOPS if args.i8_base else BF16_PEAK_TFLOPS
     for gk in ("gemm", "gemm_bgmv_shrink"):
         if gk in kern:
             kern[gk]["TFLOPs"] = gemm_flops / (kern[gk]["avg_us"] * 1e-6) / 1e12
-            kern[gk]["frac_mfma_peak"] = kern[gk]["TFLOPs"] / BF16_PEAK_TFLOPS
+            kern[gk]["frac_mfma_peak"] = kern[gk]["TFLOPs"] / mfma_peak
     dk = [k for k in ("bgmv_shrink", "bgmv_expand", "sgmv_shrink", "sgmv_expand") if k in kern]
     delta = None
     if dk:
@@ -371,10 +394,10 @@ def main():
         delta = {"kernels": dk, "us": us, "alg_bytes": byt, "GBps": byt / (us * 1e-6) / 1e9,
                  "frac_hbm_peak": byt / (us * 1e-6) / 1e9 / HBM_PEAK_GBS, "distinct_adapters": dist}
     dom = max(kern, key=lambda k: kern[k]["avg_us"])
-    traffic = None if args.fp8_base else measured_traffic(cfg, dom)
+    traffic = None if args.fp8_base or args.i8_base else measured_traffic(cfg, dom)
     if dom == "gemm" and cfg == "c4":
-        roof = {"bound": "mfma", "achieved": kern[dom]["TFLOPs"], "peak": BF16_PEAK_TFLOPS, "unit": "TFLOP/s",
-                "frac": kern[dom]["TFLOPs"] / BF16_PEAK_TFLOPS, "traffic": traffic, "kernel": dom}
+        roof = {"bound": "mfma", "achieved": kern[dom]["TFLOPs"], "peak": mfma_peak, "unit": "TFLOP/s",
+                "frac": kern[dom]["TFLOPs"] / mfma_peak, "traffic": traffic, "kernel": dom}
     else:
         roof = {"bound": "hbm", "achieved": kern[dom]["GBps"], "peak": HBM_PEAK_GBS, "unit": "GB/s",
                 "frac": kern[dom]["GBps"] / HBM_PEAK_GBS, "traffic": traffic, "kernel": dom}
@@ -383,10 +406,11 @@ def main():
         roof["alg_bytes"] = kern[dom]["alg_bytes"]
     out = {"metric": METRIC, "value": tok_s, "unit": "tokens/s", "n_gpus": 1, "steps": args.steps,
            "warmup": args.warmup, "ms_per_step": ms_step, "higher_is_better": True, "scaling": "weak",
-           "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+           "vs_baseline": None, "dtype": "int8 base, bf16 adapters" if args.i8_base else "bf16", "data": "synthetic",
            "config": {"workload": WORKLOADS[cfg] + (", base weight as E4M3 codes with a scale per output channel"
-                                                     if args.fp8_base else ""),
-                      "name": cfg + ("_fp8base" if args.fp8_base else ""), "tokens_per_step": T, "layer_copies": R,
+                                                     if args.fp8_base else ", base weight and rows as 8-bit integers"
+                                                     if args.i8_base else ""),
+                      "name": cfg + ("_fp8base" if args.fp8_base else "_i8base" if args.i8_base else ""), "tokens_per_step": T, "layer_copies": R,
                       "batches": NB, "parallelism": "none (1 GPU)"},
            "roofline": roof, "kernels": kern, "delta": delta, "kernel_timing": KERNEL_TIMING}
     if not args.no_cpu_baseline:
@@ -749,6 +773,52 @@ def run_peaks(args):
     if args.json_out:
         with open(args.json_out, "a") as f:
             f.write(line + "\n")
+
+
+def run_i8_mlp(args):
+    """A feed-forward block of Llama-7B's widths (4096, 11008) in 8-bit integers, without adapters: per step the norm
+    of the residual stream with its 8-bit form, the gated product, the 8-bit form of its rows, and the down product,
+    over weights cycled so that each step reads them from HBM."""
+    import torch
+
+    import heterogeneous_adapter_gemm_amd as hg
+    d, f, sets = 4096, 11008, 6
+    g = torch.Generator(device="cuda").manual_seed(0)
+
+    def weight(n, k):
+        code = (torch.randn((n, k), generator=g, device="cuda") * 30).round().clamp(-127, 127).to(torch.int8)
+        return code, torch.rand(n, generator=g, device="cuda") * 1e-3 + 2e-4
+
+    w = [(weight(f, d), weight(f, d), weight(d, f)) for _ in range(sets)]
+    nw = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    points = []
+    for rows in (1, 64, 2961):
+        mk = lambda k, dtype=torch.bfloat16: torch.zeros((rows, k), dtype=dtype, device="cuda")  # noqa: E731
+        stream, x = (torch.randn((rows, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+        total, c8, gated, g8 = mk(d), mk(d, torch.int8), mk(f), mk(f, torch.int8)
+        s8, gs8 = (torch.zeros(rows, device="cuda") for _ in range(2))
+
+        def step(i):
+            gate, up, down = w[i % sets]
+            hg.rows_norm_i8(x, nw, 1e-5, residual=stream, sum_out=total, code=c8, scale=s8)
+            hg.base_gated_i8(c8, s8, *gate, *up, gated, rows, f, d)
+            hg.rows_act_i8(gated, code=g8, scale=gs8)
+            hg.base_gemm_i8(g8, gs8, *down, x, rows, d, f)
+
+        steps = 200 if rows > 1000 else 1000
+        for i in range(steps // 10):
+            step(i)
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        for i in range(steps):
+            step(i)
+        torch.cuda.synchronize()
+        us = (time.perf_counter() - t0) * 1e6 / steps
+        points.append({"rows": rows, "us_per_step": us, "weight_GBps": 3 * d * f / us / 1e3,
+                       "TOPs": 6 * rows * d * f / us / 1e6})
+        log(f"{rows} rows: {us:.1f} us a block")
+    print(json.dumps({"block": "feed-forward 4096 -> 11008 -> 4096 in 8-bit integers: norm, gated product, form, down",
+                      "points": points}), flush=True)
 
 
 def run_gemm_vs_library(args):

@@ -119,6 +119,15 @@ def test_rows_of_tensors_are_checked():
         hg.base_gated_i8(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 4, 64, 64, act="tanh")
 
 
+def test_the_generators_weight():
+    from workloads import make_workload
+    wl = make_workload("c1")
+    code, scale = wl.w0_i8()
+    w = wl.w0().astype(np.float64)      # (the tiny layer's weight is fp32: the draw itself)
+    assert code.dtype == np.int8 and np.all(np.abs(code).max(1) == 127)
+    assert np.all(np.abs(w - scale[:, None].astype(np.float64) * code) <= 0.5 * scale[:, None] * (1 + 2.0 ** -20))
+
+
 def test_packed_rows_are_the_structs():
     for packed, c in ((_lib._NORM_ROWS, hg.lora_norm_rows), (_lib._ACT_ROWS, hg.lora_act_rows)):
         v = [3, 40, 5] + list(range(1 << 40, (1 << 40) + len(c._fields_) - 3))

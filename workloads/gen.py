@@ -223,6 +223,20 @@ class Workload:
             return np.ascontiguousarray(codes), scale
         return self._get(("w0fp8", layer, proj), make)
 
+    def w0_i8(self, layer: int = 0, proj: int = 0) -> Tuple[np.ndarray, np.ndarray]:
+        """The base weight as an 8-bit integer base: codes int8 [d_out, d_in] and an fp32 scale per output row
+        (largest |w| of the row maps to 127), from the same fp32 draw the bf16 base rounds; the codes are the
+        nearest (ties to even) of w / scale."""
+        c = _CFG_NO[self.name]
+        di, do = self.d_in[proj], self.d_out[proj]
+
+        def make():
+            w = _normal(do * di, self.w0_std, (self.seed, c, _T_W0, layer, proj), False).reshape(do, di)
+            amax = np.abs(w).max(axis=1).astype(np.float32)
+            scale = np.where(amax > 0, amax / np.float32(127.0), np.float32(1.0)).astype(np.float32)
+            return np.clip(np.rint(w / scale[:, None]), -127, 127).astype(np.int8), scale
+        return self._get(("w0i8", layer, proj), make)
+
     def x(self, layer: int = 0, proj: int = 0) -> np.ndarray:
         """Layer input [T, d_in] for a projection; projections that share an
         input (q, k, v read the attention block's input; gate, up the MLP
