@@ -552,15 +552,17 @@ Choice choose(const I8Args& g, bool two, bool seg) {
     Choice best{};
     double us = 1e30;
     for (const Kind& k : kKinds) {
-        if (k.stream ? seg || g.M > 256 || (two && k.bn % 32 != 0) : g.M <= 64 && !seg) continue;
+        const int64_t tiles = tiles_of(g, k, two);
+        // more rows than decode has, of few outputs: the stream's smaller tiles where they are one round (us, beside the long
+        // ones': 860 x 336 x 9376 16.5 and 22.9, 1,000 x 256 x 11008 15.5 and 19.3, 2,961 x 64 x 4096 6.7 and 9.2)
+        if (k.stream ? seg || (g.M > 256 && tiles > cus) || (two && k.bn % 32 != 0) : g.M <= 64 && !seg) continue;
         // rows of x beside those that exist would only be read past
         if (k.stream && k.bm >= 32 && g.M <= k.bm / 2) continue;
-        const int64_t tiles = tiles_of(g, k, two);
         const double one = round_us(k, g.K);
         double t = one * (double)((tiles + cus - 1) / cus);
-        // the stream's tiles of 64 x 64 are the better ones of this size from K = 8192 on (256 x 4096: 26.4 us against 27.9 at
-        // K = 11008, 12.8 against 11.8 at 4096)
-        if (k.bm == 64 && k.bn == 64 && k.stream == (g.K < 8192)) t += 0.01;
+        // the stream's tiles of as many lines as 64 x 64 are the better ones from K = 8192 on (256 x 4096: 26.4 us against
+        // 27.9 at K = 11008, 12.8 against 11.8 at 4096; gated 300 x 4096 -> 1024 in 32 x 96 9.9 against 9.3)
+        if (k.bm + k.bn == 128 && k.stream == (g.K < 8192)) t += 0.01;
         if (t < us) {
             us = t;
             best = {k, 0, 1, 1};

@@ -47,7 +47,8 @@ SHAPES = [(1, 4, 16), (1, 4096, 4096), (3, 100, 48), (16, 4160, 1040), (17, 36, 
           (257, 64, 16), (300, 272, 656), (700, 4100, 304), (1000, 4096, 512), (2049, 8100, 272), (2961, 4096, 4096), (1100, 13000, 208),
           (1500, 11008, 336), (4100, 4360, 160), (4352, 4128, 320), (2816, 6300, 592),
           (1, 17036, 272), (33, 12316, 272), (19, 8472, 272), (8429, 72, 272), (151, 16500, 272), (206, 18732, 272),
-          (342, 48388, 608), (386, 43812, 944), (391, 70364, 288), (1167, 14356, 800), (754, 21900, 560)]
+          (342, 48388, 608), (386, 43812, 944), (391, 70364, 288), (1167, 14356, 800), (754, 21900, 560),
+          (67, 6436, 272), (860, 340, 1040), (2961, 64, 528), (1000, 260, 9376), (3000, 36, 400)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -73,7 +74,8 @@ GATED = [(1, 4, 16), (1, 11008, 4096), (16, 100, 48), (20, 4100, 400), (32, 2060
          (130, 1000, 768), (256, 4100, 656), (257, 132, 16), (700, 4100, 304), (1000, 2048, 512), (2049, 4060, 272), (2961, 2048, 2048),
          (1100, 6500, 208), (1500, 5504, 336), (2816, 3156, 592), (4352, 2064, 320),
          (1, 4148, 288), (17, 4216, 272), (33, 4300, 304), (34, 6264, 320), (8903, 36, 272), (163, 8552, 272),
-         (1026, 8052, 608), (388, 21844, 960), (385, 35172, 288), (471, 17564, 800), (758, 10884, 560)]
+         (1026, 8052, 608), (388, 21844, 960), (385, 35172, 288), (471, 17564, 800), (758, 10884, 560),
+         (67, 6436, 272), (300, 1020, 304), (2961, 64, 528), (600, 516, 8208)]
 
 
 @pytest.mark.parametrize("M,N,K", GATED)
