@@ -26,10 +26,10 @@ struct I8Args {
 
 // N % 4 == 0, K % 16 == 0, and the sizes above
 bool gemm_i8_ok(int64_t M, int64_t N, int64_t K);
-// With seg, batches of more than 256 rows add the segments' LoRA expand before rounding and set *fused.
+// With seg (segments with adapters) the product adds their LoRA expand before rounding and sets *fused.
 hipError_t launch_gemm_i8(const I8Args& g, const LoraArgs* seg, bool* fused, hipStream_t s);
 hipError_t launch_gemm_i8_gated(const I8Args& g, int act, hipStream_t s);
-// Decode batches (M <= 64, a.n_su > 0): as launch_gemm_shrink (raw_mask as there).
+// Decode batches (a.n_su > 0): as launch_gemm_shrink; with more than 64 rows raw_mask is 0 and row_slot names the adapter rows.
 bool gemm_i8_shrink_fits(int64_t M, int64_t N, int64_t K, int n_su);
 hipError_t launch_gemm_i8_shrink(const I8Args& g, uint64_t raw_mask, const LoraArgs& a, const void* cp_src, void* cp_dst,
                                  int64_t cp_n, hipStream_t s);

@@ -228,7 +228,7 @@ __global__ __launch_bounds__(256, 1) void i8_stream_kernel(I8Args g) {
     i8_stream_tile<C, ACT>(g, blockIdx.x, gridDim.x, 0);
 }
 
-// Decode batches of up to 64 rows with adapters: the product's tiles, the BGMV shrink's units and the copy
+// Decode batches with adapters: the product's tiles, the BGMV shrink's units and the copy
 // of a plan's index in one launch (blocks [0, n_gemm) are tiles, then the shrink units, then kCopyBlocks
 // copying cp_n index words), as for the other bases.
 template <class C>
@@ -668,11 +668,21 @@ hipError_t launch_gemm_i8_gated(const I8Args& g, int act, hipStream_t s) {
     }
 }
 
-bool gemm_i8_shrink_fits(int64_t M, int64_t N, int64_t K, int n_su) { return M <= 64 && n_su > 0 && gemm_i8_ok(M, N, K); }
+// Up to 64 rows; and more of them while the small tiles, two workgroups a compute unit, are at most three a compute unit
+// (more than 192 rows: two): the launch saved and the shrink's units beside the tiles are worth more than the larger
+// tiles of a launch of their own.  us of the layer in one shared launch and in two: 107 x 272 -> 2800 15.4 and 18.4, 160 x 4096 -> 4096
+// 21.0 and 25.5, 90 x 4096 -> 11008 23.8 and 29.1, 192 x 4096 -> 4096 29.0 and 32.1, 250 x 4096 -> 1024 15.9 and 18.4; beyond the
+// rule, 128 x 4096 -> 11008 34.1 and 35.2, 256 x 4096 -> 4096 25.9 and 25.8, 256 x 11008 -> 4096 55.7 and 49.6.
+bool gemm_i8_shrink_fits(int64_t M, int64_t N, int64_t K, int n_su) {
+    if (n_su <= 0 || !gemm_i8_ok(M, N, K)) return false;
+    return M <= 64 || (M <= 256 && (M + 31) / 32 * ((N + 47) / 48) <= (M <= 192 ? 3 : 2) * gemm_cu_count());
+}
 
 hipError_t launch_gemm_i8_shrink(const I8Args& g0, uint64_t raw_mask, const LoraArgs& a, const void* cp_src, void* cp_dst,
                                  int64_t cp_n, hipStream_t s) {
-    if (!gemm_i8_shrink_fits(g0.M, g0.N, g0.K, a.n_su) || cp_n < 0 || cp_n > INT32_MAX) return hipErrorInvalidValue;
+    // (raw_mask: the adapter rows of at most 64; more are known by row_slot)
+    if (!gemm_i8_shrink_fits(g0.M, g0.N, g0.K, a.n_su) || cp_n < 0 || cp_n > INT32_MAX || (g0.M > 64 && raw_mask != 0))
+        return hipErrorInvalidValue;
     I8Args g = g0;
     if (raw_mask != 0) g.row_slot = nullptr;
     const int ncp = cp_n > 0 ? kCopyBlocks : 0;
@@ -692,9 +702,12 @@ hipError_t launch_gemm_i8_shrink(const I8Args& g0, uint64_t raw_mask, const Lora
     } else if (g.M <= 32) {
         if (blocks <= cus) go(StreamCfg<2, 1, 3>{});
         else go(StreamCfg<2, 3, 2>{});
-    } else {
+    } else if (g.M <= 64) {
         if (blocks <= cus) go(StreamCfg<2, 2, 2>{});
         else go(StreamCfg<4, 3, 2>{});
+    } else {
+        if ((g.M + 31) / 32 * ((g.N + 31) / 32) <= 2 * cus) go(StreamCfg<2, 2, 2>{});
+        else go(StreamCfg<2, 3, 2>{});
     }
     return hipGetLastError();
 }

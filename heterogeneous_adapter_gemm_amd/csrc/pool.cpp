@@ -1448,7 +1448,9 @@ int linear_impl(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t n, c
         ia.K = a.d_in;
     }
     const PlanStage& ps = p->pstage[plan->stage];
-    if (first && !gemm_done) {
+    // (a shared launch of up to 64 rows reads a plan's new index where it is, and copies it beside its work)
+    const bool copies = first && gemm_done && T <= 64;
+    if (first && !copies) {
         // (a batch without adapter rows reads no index)
         if (any && (e = launch_upload(ps.host_dev, base, plan->words, st)) != hipSuccess)
             return fail(LORA_EHIP, "plan upload: %s", hipGetErrorString(e));
@@ -1459,7 +1461,7 @@ int linear_impl(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t n, c
         // its device mapping) and stores it in the ring entry in the same launch
         LoraArgs ah = a;
         const int32_t* rsh = rs;
-        if (first) {
+        if (copies) {
             const uint8_t* hb = static_cast<const uint8_t*>(ps.host_dev);
             auto H = [&](int64_t off) { return reinterpret_cast<const int32_t*>(hb) + off; };
             ah.g_slot = H(L.g_slot);
@@ -1479,14 +1481,15 @@ int linear_impl(lora_pool* p, const lora_plan* plan, int32_t layer, int32_t n, c
             ah.t_row0 = H(L.t_row0);
             rsh = H(L.row_slot);
         }
-        // rows with an adapter (at most 64 rows here): the decode rows in the plan's groups
+        // rows with an adapter (of at most 64 rows; with more, the index in the ring entry names them): the decode rows in
+        // the plan's groups
         uint64_t raw_mask = 0;
         if (T <= 64)
             for (int32_t r : plan->rows) raw_mask |= uint64_t(1) << r;
         e = timed_launch(p, LORA_K_GEMM_BGMV_SHRINK, st, [&] {
-            const void* cps = first ? ps.host_dev : nullptr;
-            void* cpd = first ? base : nullptr;
-            const int64_t cpn = first ? plan->words : 0;
+            const void* cps = copies ? ps.host_dev : nullptr;
+            void* cpd = copies ? base : nullptr;
+            const int64_t cpn = copies ? plan->words : 0;
             if (i8) {
                 ia.row_slot = rsh;
                 return launch_gemm_i8_shrink(ia, raw_mask, ah, cps, cpd, cpn, st);

@@ -181,7 +181,8 @@ def dev(v):
 
 @pytest.mark.parametrize("n,d_in,d_out,n_ad", [(1, 528, 24, 1), (5, 512, 272, 3), (16, 1040, 4360, 16), (17, 640, 264, 2), (32, 512, 8200, 6),
                                                (64, 4096, 4096, 16), (64, 512, 10248, 4), (50, 2064, 16392, 9), (65, 528, 1000, 8),
-                                               (200, 1040, 1032, 5), (256, 512, 4096, 64), (300, 512, 520, 7), (1000, 784, 1032, 12)])
+                                               (200, 1040, 1032, 5), (256, 512, 4096, 64), (300, 512, 520, 7), (1000, 784, 1032, 12),
+                                               (90, 272, 8208, 7), (192, 528, 5512, 40), (130, 4096, 520, 130)])
 def test_decode_rows_with_adapters(n, d_in, d_out, n_ad):
     import heterogeneous_adapter_gemm_amd as hg
     say("decode rows", n, d_in, d_out, n_ad)
@@ -209,8 +210,7 @@ def test_decode_rows_with_adapters(n, d_in, d_out, n_ad):
     hg.lora_plan_destroy(plan)
 
 
-# segments with and without an adapter, empty ones, of one row, ending inside a tile; with and without decode rows;
-# up to 256 rows in all (the expand of its own) and more (in the product's epilogue)
+# segments with and without an adapter, empty ones, of one row, ending inside a tile; with and without decode rows
 @pytest.mark.parametrize("lens,n_dec,d_in,d_out", [([1], 0, 512, 264), ([30, 0, 7], 9, 528, 1032), ([100, 77, 1], 40, 1040, 520),
                                                    ([130, 1, 0, 77], 145, 1024, 1040), ([300, 212], 0, 512, 4104), ([64, 700, 33, 400], 192, 784, 2056),
                                                    ([1024, 900, 61], 64, 512, 4096), ([513, 1, 1, 640], 7, 4096, 1048)])
