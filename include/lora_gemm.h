@@ -428,7 +428,8 @@ typedef struct lora_norm_rows {
  *   p = h * weight (exact in fp32),  r = 1 / sqrt(mean h^2 + eps)
  *   y = p r, rounded to bf16 once;  code and scale the 8-bit form of p r, where the codes are those of p (r is the
  *   row's own factor and cancels): they depend on no rounding of y or r.  scale = max |p| r / 127.
- * Sums are fp32: a row whose sum of squares passes fp32's range is NaN, as one that holds an infinity or NaN.
+ * Sums are fp32: a row whose sum of squares passes fp32's range is NaN, as one that holds an infinity or NaN; a row
+ * with a p beyond that range has scale NaN, codes 0 and infinities in y.
  * n_rows = 0 is a no-op.  Errors: EINVAL, EHIP. */
 int rows_norm_i8(const lora_norm_rows* rows, void* stream);
 

@@ -169,6 +169,24 @@ def test_squares_past_the_range_are_nan():
     assert bool(torch.isnan(y[0]).all()) and bool(torch.isnan(scale[0])) and bool((y[1] == 1).all()) and bool((code[1] == 127).all())
 
 
+@pytest.mark.parametrize("d", [8, 136, 4096, 65536])
+def test_products_past_the_range(d):
+    """Squares that fit, times a weight that does not: infinities in y, and no codes; the rows beside are not touched by it."""
+    import heterogeneous_adapter_gemm_amd as hg
+    x = torch.ones((3, d), dtype=torch.bfloat16, device="cuda")
+    x[1, d - 1] = 2.0 ** 50
+    w = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    w[d - 1] = 2.0 ** 100
+    y, held = torch.zeros_like(x), torch.zeros_like(x)
+    code, scale = torch.full((3, d), 5, dtype=torch.int8, device="cuda"), torch.zeros(3, device="cuda")
+    hg.rows_norm_i8(x, w, 1e-5, y=y, code=code, scale=scale, held=held)
+    torch.cuda.synchronize()
+    assert bool(torch.isinf(y[1, d - 1])) and bool(torch.isfinite(y[1, :d - 1]).all()) and bool(torch.isfinite(y[0]).all())
+    assert bool(torch.isnan(scale[1])) and bool((code[1] == 0).all()) and bool(torch.isnan(held[1]).all())
+    for t in (0, 2):
+        assert int(code[t, d - 1]) == 127 and bool((code[t, :d - 1] == 0).all()) and bool(torch.isfinite(scale[t]))
+
+
 @pytest.mark.parametrize("d", [64, 4096])
 def test_some_outputs_only_and_in_place(d):
     import heterogeneous_adapter_gemm_amd as hg
