@@ -429,7 +429,7 @@ typedef struct lora_norm_rows {
  *   y = p r, rounded to bf16 once;  code and scale the 8-bit form of p r, where the codes are those of p (r is the
  *   row's own factor and cancels): they depend on no rounding of y or r.  scale = max |p| r / 127.
  * Sums are fp32: a row whose sum of squares passes fp32's range is NaN, as one that holds an infinity or NaN; a row
- * with a p beyond that range has scale NaN, codes 0 and infinities in y.
+ * with a p beyond that range has scale NaN, codes 0 and infinities in y, one with a p r beyond it an infinite scale.
  * n_rows = 0 is a no-op.  Errors: EINVAL, EHIP. */
 int rows_norm_i8(const lora_norm_rows* rows, void* stream);
 
